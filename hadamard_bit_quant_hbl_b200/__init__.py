@@ -25,6 +25,8 @@ __all__ = [
     "hbl_norm_fht_quant", "hbl_ternary_gemm",
     "hbl_forward_workspace", "hbl_forward", "hbl_forward_decode", "codes_row_bytes",
     "hbl_qkv_codes_bytes", "hbl_qkv_quant", "hbl_qkv_dequant",
+    "hbl_kv_cache_bytes", "hbl_kv_append", "hbl_kv_gather",
+    "hbl_attn_decode_workspace", "hbl_attn_decode", "hbl_attn_prompt",
 ]
 
 HBL_OK, HBL_EINVAL, HBL_EUNSUPPORTED, HBL_ECUDA, HBL_ETIMEOUT = range(5)
@@ -65,6 +67,19 @@ _SIGNATURES = {
     "hbl_qkv_quant": (_c_int, [_c_void_p, _c_size_t, _c_void_p, _c_float, _c_int, _c_int, _c_int, _c_int, _c_void_p,
                                _c_size_t, _c_void_p, _c_void_p]),
     "hbl_qkv_dequant": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p]),
+    "hbl_kv_cache_bytes": (_c_size_t, [_c_int] * 5),
+    "hbl_kv_append": (_c_int, [_c_void_p, _c_size_t, _c_void_p, _c_size_t, _c_void_p, _c_size_t, _c_void_p, _c_void_p,
+                               _c_float, _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_size_t, _c_int, _c_int,
+                               _c_void_p, _c_size_t, _c_void_p]),
+    "hbl_kv_gather": (_c_int, [_c_void_p, _c_size_t, _c_int, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                               _c_void_p, _c_void_p, _c_void_p]),
+    "hbl_attn_decode_workspace": (_c_size_t, [_c_int] * 4),
+    "hbl_attn_decode": (_c_int, [_c_void_p, _c_size_t, _c_void_p, _c_size_t, _c_int, _c_int, _c_void_p, _c_int,
+                                 _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_size_t,
+                                 _c_void_p, _c_void_p, _c_void_p]),
+    "hbl_attn_prompt": (_c_int, [_c_void_p, _c_size_t, _c_void_p, _c_size_t, _c_void_p, _c_size_t, _c_void_p, _c_void_p,
+                                 _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_int, _c_void_p,
+                                 _c_void_p, _c_void_p]),
     "hbl_forward": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_float, _c_int, _c_int, _c_int,
                              _c_int, _c_int, _c_float, _c_float, _c_void_p, _c_size_t, _c_void_p, _c_int,
                              _c_void_p]),
@@ -312,3 +327,172 @@ def hbl_qkv_dequant(codes, gamma, D: int, bits: int, Y=None, stream=None):
     _check(lib().hbl_qkv_dequant(_ptr(codes), _ptr(gamma), M, H, D, bits, _ptr(Y), _stream(stream, codes)),
            "hbl_qkv_dequant")
     return Y
+
+
+def _rows(X, what: str):
+    """(pointer, elements between tokens) of bf16 states [T, H, D] whose token rows may lie apart
+    (a slice of a fused projection output); the heads of a token must be dense."""
+    import torch
+
+    if X.dim() != 3 or X.dtype != torch.bfloat16:
+        raise ValueError(f"expected bf16 {what} [tokens, heads, D]")
+    if not X.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    T, H, D = X.shape
+    st = X.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"expected dense heads in {what}")
+    return X.data_ptr(), st[0] if T > 1 else H * D
+
+
+def _ints(t, n: int, like, what: str):
+    """Pointer of a contiguous int32 tensor of n entries on the device of `like`."""
+    import torch
+
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"expected int32 {what} of {n} entries")
+    _same_device(t, like)
+    return _ptr(t)
+
+
+def _same_device(t, like) -> None:
+    if t.device != like.device:
+        raise ValueError("expected tensors on one device")
+
+
+def _out(t, shape, dtype, like, what: str):
+    """A given output of this shape and type, or a new one."""
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"expected {what} of shape {tuple(shape)} and type {dtype}")
+    _same_device(t, like)
+    return t
+
+
+def _call(f, name: str, like, args, stream) -> None:
+    """The library call with the tensors' device current (its streams and launches belong to it)."""
+    import torch
+
+    if torch.cuda.current_device() != like.device.index:
+        with torch.cuda.device(like.device):
+            status = f(*args, _stream(stream, like))
+    else:
+        status = f(*args, _stream(stream, like))
+    if status != HBL_OK:
+        raise HblError(status, name)
+
+
+def hbl_kv_cache_bytes(num_pages: int, page_size: int, Hkv: int, D: int, bits: int) -> int:
+    return lib().hbl_kv_cache_bytes(num_pages, page_size, Hkv, D, bits)
+
+
+def _num_pages(cache, page_size: int, Hkv: int, D: int, bits: int) -> int:
+    """Whole pages that the cache buffer (uint8) holds."""
+    import torch
+
+    if cache.dtype != torch.uint8:
+        raise ValueError("expected a uint8 cache buffer")
+    page = max(1, Hkv * (page_size // 16) * (4 * D * bits + 128))
+    return min(cache.numel() // page, 0x7FFFFFFF // max(1, page_size))
+
+
+def hbl_kv_append(K, V, slots, cache, page_size: int, bits: int = 3, pos=None, rope_theta: float = 10000.0, Q=None,
+                  q_out=None, stream=None):
+    """Write bf16 K, V [T, Hkv, D] into the paged cache (uint8 buffer of hbl_kv_cache_bytes) at `slots`
+    (int32 [T]), quantised per head, K rotated when `pos` (int32 [T]) is given. With Q [T, Hq, D],
+    returns Q rotated, bf16 (q_out may be Q itself); K, V and Q may be slices of a fused QKV output."""
+    import torch
+
+    T, Hkv, D = K.shape
+    if V.shape != K.shape:
+        raise ValueError("expected K and V of one shape")
+    kp, ks = _rows(K, "K")
+    vp, vs = _rows(V, "V")
+    _same_device(V, K)
+    _same_device(cache, K)
+    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if Q is not None:
+        if Q.shape[0] != T or Q.shape[2] != D:
+            raise ValueError("expected Q with the tokens and the head size of K")
+        qp, qs = _rows(Q, "Q")
+        _same_device(Q, K)
+        Hq = Q.shape[1]
+        q_out = _out(q_out, Q.shape, torch.bfloat16, K, "q_out")
+        op, os_ = _rows(q_out, "q_out")
+    _call(lib().hbl_kv_append, "hbl_kv_append", K,
+          (qp, qs, kp, ks, vp, vs, None if pos is None else _ints(pos, T, K, "pos"), _ints(slots, T, K, "slots"),
+           float(rope_theta), T, Hq, Hkv, D, bits, _ptr(cache), cache.numel(),
+           _num_pages(cache, page_size, Hkv, D, bits), page_size, op, os_), stream)
+    return q_out
+
+
+def hbl_kv_gather(cache, slots, Hkv: int, D: int, page_size: int, bits: int = 3, K=None, V=None, stream=None):
+    """The cached tokens at `slots` (int32 [T]) as bf16 (K, V) [T, Hkv, D]."""
+    import torch
+
+    T = slots.numel()
+    K = _out(K, (T, Hkv, D), torch.bfloat16, cache, "K")
+    V = _out(V, (T, Hkv, D), torch.bfloat16, cache, "V")
+    _call(lib().hbl_kv_gather, "hbl_kv_gather", cache,
+          (_ptr(cache), cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
+           _ints(slots, T, cache, "slots"), T, Hkv, D, bits, _ptr(K), _ptr(V)), stream)
+    return K, V
+
+
+def hbl_attn_decode_workspace(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return lib().hbl_attn_decode_workspace(B, Hq, Hkv, D)
+
+
+def hbl_attn_decode(Q, cache, tables, lens, Hkv: int, page_size: int, bits: int = 3, scale=None, workspace=None, O=None,
+                    lse=None, stream=None):
+    """Attention of bf16 Q [B, Hq, D] (one rotated token per sequence) over the paged cache: `tables`
+    int32 [B, width] pages, `lens` int32 [B] tokens; scale defaults to 1/sqrt(D). Returns bf16
+    O [B, Hq, D]; fills lse fp32 [B, Hq] when given."""
+    import torch
+
+    B, Hq, D = Q.shape
+    qp, qs = _rows(Q, "Q")
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError("expected tables [B, width]")
+    _same_device(cache, Q)
+    if workspace is None:
+        workspace = _u8_empty(hbl_attn_decode_workspace(B, Hq, Hkv, D), Q.device)
+    _same_device(workspace, Q)
+    O = _out(O, (B, Hq, D), torch.bfloat16, Q, "O")
+    if lse is not None:
+        _out(lse, (B, Hq), torch.float32, Q, "lse")
+    _call(lib().hbl_attn_decode, "hbl_attn_decode", Q,
+          (qp, qs, _ptr(cache), cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
+           _ints(tables, tables.numel(), Q, "tables"), tables.shape[1], _ints(lens, B, Q, "lens"), B, Hq, Hkv, D, bits,
+           float(D ** -0.5 if scale is None else scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+           _ptr(O), _ptr(lse)), stream)
+    return O
+
+
+def hbl_attn_prompt(Q, K, V, cu_q, cu_k, max_q=None, scale=None, causal: bool = True, O=None, lse=None, stream=None):
+    """Attention over packed prompts: bf16 Q [total_q, Hq, D], K and V [total_k, Hkv, D], int32 cu_q and
+    cu_k [B + 1] borders; max_q bounds the longest prompt's queries (default total_q); scale defaults
+    to 1/sqrt(D). Returns bf16 O [total_q, Hq, D]; fills lse fp32 [total_q, Hq] when given."""
+    import torch
+
+    Tq, Hq, D = Q.shape
+    Tk, Hkv, _ = K.shape
+    if V.shape != K.shape or K.shape[2] != D:
+        raise ValueError("expected K and V of one shape, with the head size of Q")
+    qp, qs = _rows(Q, "Q")
+    kp, ks = _rows(K, "K")
+    vp, vs = _rows(V, "V")
+    _same_device(K, Q)
+    _same_device(V, Q)
+    B = cu_q.numel() - 1
+    O = _out(O, (Tq, Hq, D), torch.bfloat16, Q, "O")
+    if lse is not None:
+        _out(lse, (Tq, Hq), torch.float32, Q, "lse")
+    _call(lib().hbl_attn_prompt, "hbl_attn_prompt", Q,
+          (qp, qs, kp, ks, vp, vs, _ints(cu_q, B + 1, Q, "cu_q"), _ints(cu_k, B + 1, Q, "cu_k"), B, Tq, Tk,
+           Tq if max_q is None else int(max_q), Hq, Hkv, D, float(D ** -0.5 if scale is None else scale), int(causal),
+           _ptr(O), _ptr(lse)), stream)
+    return O

@@ -11,10 +11,11 @@ namespace hbl {
 enum : int {
   kErrTimeout = 1,       // a bounded wait on an mbarrier or flag ran out
   kErrBadTernary = 2,    // hbl_pack_ternary saw a code outside {-1, 0, 1}
+  kErrBadIndex = 4,      // a cache slot, page number or length outside its range (skipped or cut)
 };
 
-// One flag per device (the library's module is loaded once per device context).
-__device__ int g_error_flags;
+// One flag per device and source file (the library's module is loaded once per device context).
+static __device__ int g_error_flags;
 
 __device__ __forceinline__ void raise_error(int bits) { atomicOr(&g_error_flags, bits); }
 
@@ -87,7 +88,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // Self-test of the time-out path: one thread waits on a barrier that nothing completes, with the
 // bounded loop of mbar_wait but a short limit; the wait runs out and raises the error flag.
-__global__ void selftest_timeout_kernel(uint64_t limit_ns) {
+static __global__ void selftest_timeout_kernel(uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);

@@ -15,6 +15,7 @@
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
 #include "gemm_swap.cuh"
+#include "host.cuh"
 #include "norm_fht_quant.cuh"
 #include "norm_fht_quant_tc.cuh"
 #include "norm_fht_quant_tc2.cuh"
@@ -25,61 +26,15 @@
 using namespace hbl;
 
 namespace {
-
 thread_local int t_last_cuda_error = 0;
+}
 
-hbl_status cuda_fail(cudaError_t e) {
+hbl_status hbl::cuda_fail(cudaError_t e) {
   t_last_cuda_error = (int)e;
   return HBL_ECUDA;
 }
 
-#define HBL_CHECK_LAUNCH()                          \
-  do {                                              \
-    const cudaError_t e_ = cudaGetLastError();      \
-    if (e_ != cudaSuccess) return cuda_fail(e_);    \
-  } while (0)
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-inline bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
-
-constexpr int kMaxDevices = 64;
-
-int device_sms(int dev) {
-  static int cache[kMaxDevices] = {0};
-  if (dev < 0 || dev >= kMaxDevices) return 148;
-  if (cache[dev] == 0) {
-    int v = 0;
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    cache[dev] = v > 0 ? v : 148;
-  }
-  return cache[dev];
-}
-
-// Raise a kernel's dynamic shared memory limit when a launch needs more than was allowed so far
-// on the current device (the limit does not change occupancy; the launch's own size does). The
-// default limit counts static shared memory too, so it is raised for any non-zero size.
-struct SmemLimit {
-  std::mutex mu;
-  int allowed[64] = {0};
-};
-
-template <typename F>
-cudaError_t allow_smem(F* kernel, int bytes, SmemLimit& lim) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  dev &= 63;
-  std::lock_guard<std::mutex> lk(lim.mu);
-  if (lim.allowed[dev] >= bytes) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  // the kernels stream their data, so L1 matters less than shared memory: ask for the largest
-  // carveout, so that the occupancy query (which sizes the persistent grids) and the launch agree
-  // on how many CTAs share an SM
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) lim.allowed[dev] = bytes;
-  return e;
-}
+namespace {
 
 // ---------------------------------------------------------------- packed-weight layout
 
@@ -439,19 +394,6 @@ hbl_status run_decode(const DecodeArgs& a0, bool fused, cudaStream_t s) {
   return HBL_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // 2-D K-major int8 operand [rows][K] as a TMA map with a (128 bytes x box_rows) box, 128-byte swizzle.
 bool make_map_i8(CUtensorMap* map, const void* base, int K, int rows, int box_rows) {
   auto enc = get_encode_fn();
@@ -791,8 +733,12 @@ hbl_status hbl_device_status(hbl_stream_t stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e);
   }
+  int more = 0;
+  const hbl_status st = attn_take_errors(s, &more);
+  if (st != HBL_OK) return st;
+  flags |= more;
   if (flags & kErrTimeout) return HBL_ETIMEOUT;
-  if (flags & kErrBadTernary) return HBL_EINVAL;
+  if (flags & (kErrBadTernary | kErrBadIndex)) return HBL_EINVAL;
   return HBL_OK;
 }
 

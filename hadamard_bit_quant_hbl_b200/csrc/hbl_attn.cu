@@ -1,0 +1,217 @@
+// C ABI of the low-bit key-value cache and of the attention over it (declared in include/hbl.h):
+// argument checks, kernel selection and launches, as in hbl.cu.
+#include <math.h>
+
+#include "hbl.h"
+
+#include "attn_decode.cuh"
+#include "attn_prompt.cuh"
+#include "common.cuh"
+#include "host.cuh"
+#include "kv_cache.cuh"
+
+using namespace hbl;
+
+hbl_status hbl::attn_take_errors(cudaStream_t s, int* flags) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flags, g_error_flags, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (*flags) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_error_flags, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return HBL_OK;
+}
+
+namespace {
+
+bool head_ok(int D, int bits) {
+  return (D == 64 || D == 128 || D == 256) && (bits == 2 || bits == 3 || bits == 4 || bits == 8);
+}
+
+// f(std::integral_constant<int, D>, std::integral_constant<int, bits>) for a supported pair
+template <typename F>
+hbl_status for_head(int D, int bits, F f) {
+  auto at_d = [&](auto d) {
+    switch (bits) {
+      case 2: return f(d, std::integral_constant<int, 2>());
+      case 3: return f(d, std::integral_constant<int, 3>());
+      case 4: return f(d, std::integral_constant<int, 4>());
+      default: return f(d, std::integral_constant<int, 8>());
+    }
+  };
+  if (D == 64) return at_d(std::integral_constant<int, 64>());
+  if (D == 128) return at_d(std::integral_constant<int, 128>());
+  return at_d(std::integral_constant<int, 256>());
+}
+
+// Checks of the cache's shape and buffer shared by the three calls that take one.
+hbl_status check_cache(const void* cache, size_t cache_bytes, int num_pages, int page_size, int Hkv, int D, int bits) {
+  if (!cache || num_pages < 1 || page_size < 1 || Hkv < 1 || D < 1 || bits < 1) return HBL_EINVAL;
+  if (!head_ok(D, bits) || page_size % kKvChunk != 0 || Hkv > 65535) return HBL_EUNSUPPORTED;
+  if ((long long)num_pages * page_size > 0x7fffffffll) return HBL_EUNSUPPORTED;
+  if (!aligned(cache, 16) || cache_bytes < hbl_kv_cache_bytes(num_pages, page_size, Hkv, D, bits)) return HBL_EINVAL;
+  return HBL_OK;
+}
+
+bool rows_ok(const void* X, size_t stride, int H, int D) {
+  return X && aligned(X, 16) && stride >= (size_t)H * D && stride % 8 == 0;
+}
+
+KvCacheView view(const void* cache, int num_pages, int page_size, int Hkv) {
+  return KvCacheView{static_cast<uint8_t*>(const_cast<void*>(cache)), num_pages, page_size, Hkv};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t hbl_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D, int bits) {
+  if (num_pages <= 0 || page_size <= 0 || Hkv <= 0 || D <= 0 || bits <= 0) return 0;
+  return (size_t)num_pages * Hkv * (page_size / kKvChunk) * kv_record_bytes(D, bits);
+}
+
+hbl_status hbl_kv_append(const void* Q, size_t q_stride, const void* K, size_t k_stride, const void* V, size_t v_stride,
+                         const int32_t* pos, const int32_t* slots, float rope_theta, int T, int Hq, int Hkv, int D,
+                         int bits, void* cache, size_t cache_bytes, int num_pages, int page_size, void* q_out,
+                         size_t qo_stride, hbl_stream_t stream) {
+  const hbl_status st = check_cache(cache, cache_bytes, num_pages, page_size, Hkv, D, bits);
+  if (st != HBL_OK) return st;
+  if (T < 0 || Hq < 0) return HBL_EINVAL;
+  if (pos && !(rope_theta > 1.f && rope_theta < 3.0e38f)) return HBL_EINVAL;
+  if (T == 0) return HBL_OK;
+  if (!slots || !aligned(slots, 4) || (pos && !aligned(pos, 4))) return HBL_EINVAL;
+  if (!rows_ok(K, k_stride, Hkv, D) || !rows_ok(V, v_stride, Hkv, D)) return HBL_EINVAL;
+  if (Hq > 0 && (!rows_ok(Q, q_stride, Hq, D) || !rows_ok(q_out, qo_stride, Hq, D))) return HBL_EINVAL;
+  if (Hq > 0 && Q == q_out && q_stride != qo_stride) return HBL_EINVAL;
+  KvAppendArgs a;
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.K = static_cast<const uint16_t*>(K);
+  a.V = static_cast<const uint16_t*>(V);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.pos = pos;
+  a.slots = slots;
+  a.theta = rope_theta;
+  a.T = T;
+  a.Hq = Hq;
+  a.c = view(cache, num_pages, page_size, Hkv);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.qo_stride = qo_stride;
+  const int tiles = (T + kAppendTokens - 1) / kAppendTokens;
+  const int heads = Hq + 2 * Hkv;
+  // a CTA takes more heads (and builds the table of angles for more of them) as far as the tiles
+  // alone fill the device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int want = 4 * device_sms(dev);
+  int groups = want / tiles < 1 ? 1 : want / tiles;
+  if (groups > (heads + 3) / 4) groups = (heads + 3) / 4;
+  a.heads_per_cta = (heads + groups - 1) / groups;
+  groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
+  const dim3 grid(tiles, groups);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return for_head(D, bits, [&](auto d, auto b) {
+    return pos ? launch_pdl(kv_append_kernel<d(), b(), true>, grid, dim3(kAppendThreads), 0, s, a)
+               : launch_pdl(kv_append_kernel<d(), b(), false>, grid, dim3(kAppendThreads), 0, s, a);
+  });
+}
+
+hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, int page_size, const int32_t* slots,
+                         int T, int Hkv, int D, int bits, void* K, void* V, hbl_stream_t stream) {
+  const hbl_status st = check_cache(cache, cache_bytes, num_pages, page_size, Hkv, D, bits);
+  if (st != HBL_OK) return st;
+  if (T < 0) return HBL_EINVAL;
+  if (T == 0) return HBL_OK;
+  if (!slots || !aligned(slots, 4) || (!K && !V) || !aligned(K, 16) || !aligned(V, 16)) return HBL_EINVAL;
+  KvGatherArgs a;
+  a.c = view(cache, num_pages, page_size, Hkv);
+  a.slots = slots;
+  a.T = T;
+  a.K = static_cast<uint16_t*>(K);
+  a.V = static_cast<uint16_t*>(V);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return for_head(D, bits, [&](auto d, auto b) {
+    return launch_pdl(kv_gather_kernel<d(), b()>, dim3((T + kGatherTokens - 1) / kGatherTokens, Hkv),
+                      dim3(2 * kGatherTokens * d() / 16), 0, s, a);
+  });
+}
+
+size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
+  return 256;
+}
+
+hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, size_t cache_bytes, int num_pages,
+                           int page_size, const int32_t* tables, int table_width, const int32_t* lens, int B, int Hq,
+                           int Hkv, int D, int bits, float scale, void* workspace, size_t ws_bytes, void* O, float* lse,
+                           hbl_stream_t stream) {
+  const hbl_status st = check_cache(cache, cache_bytes, num_pages, page_size, Hkv, D, bits);
+  if (st != HBL_OK) return st;
+  if (B < 0 || Hq < 1 || Hq % Hkv != 0 || table_width < 1 || !isfinite(scale)) return HBL_EINVAL;
+  if (B > kDecodeMaxB || (long long)table_width * page_size > 0x7fffffffll) return HBL_EUNSUPPORTED;
+  if (B == 0) return HBL_OK;
+  if (!rows_ok(Q, q_stride, Hq, D) || !tables || !aligned(tables, 4) || !lens || !aligned(lens, 4)) return HBL_EINVAL;
+  if (!O || !aligned(O, 16) || (lse && !aligned(lse, 4))) return HBL_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < hbl_attn_decode_workspace(B, Hq, Hkv, D)) return HBL_EINVAL;
+  DecodeAttnArgs a;
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.q_stride = q_stride;
+  a.c = view(cache, num_pages, page_size, Hkv);
+  a.tables = tables;
+  a.table_width = table_width;
+  a.lens = lens;
+  a.B = B;
+  a.Hq = Hq;
+  a.scale = scale;
+  a.O = static_cast<uint16_t*>(O);
+  a.lse = lse;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return for_head(D, bits, [&](auto d, auto b) {
+    return launch_pdl(attn_decode_kernel<d(), b()>, dim3((unsigned)(((long long)B * Hq + 3) / 4)), dim3(128), 0, s, a);
+  });
+}
+
+hbl_status hbl_attn_prompt(const void* Q, size_t q_stride, const void* K, size_t k_stride, const void* V,
+                           size_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int B, int total_q, int total_k,
+                           int max_q, int Hq, int Hkv, int D, float scale, int causal, void* O, float* lse,
+                           hbl_stream_t stream) {
+  if (B < 0 || total_q < 0 || total_k < 0 || max_q < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !isfinite(scale))
+    return HBL_EINVAL;
+  if (D < 1) return HBL_EINVAL;
+  if ((D != 64 && D != 128 && D != 256) || B > kPromptMaxB || Hq > 65535) return HBL_EUNSUPPORTED;
+  if (B == 0 || total_q == 0) return HBL_OK;
+  if (!rows_ok(Q, q_stride, Hq, D) || !cu_q || !aligned(cu_q, 4) || !cu_k || !aligned(cu_k, 4)) return HBL_EINVAL;
+  if (total_k > 0 && (!rows_ok(K, k_stride, Hkv, D) || !rows_ok(V, v_stride, Hkv, D))) return HBL_EINVAL;
+  if (!O || !aligned(O, 16) || (lse && !aligned(lse, 4))) return HBL_EINVAL;
+  PromptAttnArgs a;
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.K = static_cast<const uint16_t*>(K);
+  a.V = static_cast<const uint16_t*>(V);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.B = B;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.max_q = max_q;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.O = static_cast<uint16_t*>(O);
+  a.lse = lse;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((total_q + 3) / 4, Hq);
+  if (D == 64) return launch_pdl(attn_prompt_kernel<64>, grid, dim3(128), 0, s, a);
+  if (D == 128) return launch_pdl(attn_prompt_kernel<128>, grid, dim3(128), 0, s, a);
+  return launch_pdl(attn_prompt_kernel<256>, grid, dim3(128), 0, s, a);
+}
+
+}  // extern "C"

@@ -25,7 +25,7 @@
  *     Device-side bounded waits that give up are reported by the next
  *     hbl_device_status() call as HBL_ETIMEOUT.
  *
- * Scalar sizes: 1 <= M, 1 <= N, K a multiple of 256, K <= 32768.
+ * Scalar sizes of the layer calls: 1 <= M, 1 <= N, K a multiple of 256, K <= 32768.
  */
 #ifndef HBL_H_
 #define HBL_H_
@@ -265,6 +265,92 @@ hbl_status hbl_qkv_quant(const void* X, size_t row_stride, const int32_t* pos, f
  * nearest even. Asynchronous. */
 hbl_status hbl_qkv_dequant(const void* codes, const float* gamma, int M, int H, int D, int bits,
                            void* Y, hbl_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Paged low-bit key-value cache and the attention over it: the path from the fused QKV projection
+ * to the input of Wo. Per layer, a prompt runs hbl_kv_append, hbl_kv_gather (the states the model
+ * attends to are the quantised ones) and hbl_attn_prompt; a new token runs hbl_kv_append and
+ * hbl_attn_decode. Quantisation per token and head as in hbl_qkv_quant.
+ *
+ * The cache is one caller-owned buffer of hbl_kv_cache_bytes(...) bytes, 16-byte aligned, of
+ * num_pages pages of page_size tokens (a multiple of 16; num_pages * page_size < 2^31). Token r of
+ * page p is slot p * page_size + r. It needs no initial contents. Layout, for callers that move
+ * pages: [page][KV head][page_size / 16] records of 4 D b + 128 bytes, each holding 16 tokens:
+ *   K codes   16 rows (one per token) of D b / 8 bytes
+ *   V codes   D b / 16 units of 16 bits, each unit for the 16 tokens in turn
+ *   scales    fp32 gamma [16] of K, then [16] of V
+ * A token's bits are the little-endian bit string of hbl_qkv_quant for b = 2, 4, 8 (V unit j = its
+ * bits [16 j, 16 j + 16)). Three-bit codes go five to a half-word, at bits 0, 3, 6, 9, 12: K in
+ * groups of 32 codes, half-word h = 0..5 of the group holding codes 5h .. 5h+4 and bit i of code
+ * 30 + j being bit 15 of half-word 2i + j; V in groups of 16 codes, unit j = 0..2 of the group
+ * holding codes 5j .. 5j+4 and bit j of code 15 being its bit 15.
+ * D 64, 128 or 256; bits 2, 3, 4 or 8; page_size a multiple of 16 (else HBL_EUNSUPPORTED). A slot,
+ * page number or length outside its range is skipped (or cut to the range) on the device and makes
+ * the next hbl_device_status() return HBL_EINVAL; nothing outside the buffers is touched. */
+size_t hbl_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D, int bits);
+
+/* Write T new tokens into the cache: RoPE on K (and Q) when pos is given, then K and V quantised per
+ * head as they are stored.
+ *   Q, K, V    device bf16; token t, head h starts at element t*stride + h*D; 16-byte aligned, strides
+ *              >= heads*D and multiples of 8 (so the slices of a fused QKV output are read in place)
+ *   pos        device int32 [T] positions, or NULL for no rotation
+ *   slots      device int32 [T]; a negative slot leaves the token out of the cache. A slot may occur
+ *              once per call (the contents of one that occurs twice are unspecified)
+ *   Hq, q_out  the rotated Q rounded to bf16, rows of qo_stride elements; q_out may be Q itself with
+ *              the same stride. Hq = 0: no Q part (Q, q_out NULL)
+ * T = 0 does nothing. The codes are those of an evaluation in 64 bits: the kernel decides in fp32 and
+ * takes a head again in fp64 where a value lies within the fp32 error of a rounding boundary. The
+ * states must be finite. Asynchronous. */
+hbl_status hbl_kv_append(const void* Q, size_t q_stride, const void* K, size_t k_stride, const void* V, size_t v_stride,
+                         const int32_t* pos, const int32_t* slots, float rope_theta, int T, int Hq, int Hkv, int D,
+                         int bits, void* cache, size_t cache_bytes, int num_pages, int page_size, void* q_out,
+                         size_t qo_stride, hbl_stream_t stream);
+
+/* Read T cached tokens back, x~ = (2u - L) gamma / L rounded to bf16:
+ *   slots   device int32 [T], in any order, repeats allowed; a negative slot leaves its rows as they are
+ *   K, V    device bf16 [T][Hkv][D], 16-byte aligned; one of them may be NULL
+ * T = 0 does nothing. Asynchronous. */
+hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, int page_size, const int32_t* slots,
+                         int T, int Hkv, int D, int bits, void* K, void* V, hbl_stream_t stream);
+
+/* Attention of one token per sequence over the cache (its own K and V already appended):
+ *   o[b][h] = sum_t softmax_t(scale q . k~_t) v~_t over the first lens[b] tokens of sequence b, head h
+ *   of Hq reading KV head h / (Hq / Hkv); lens[b] = 0 gives o = 0 and lse = -inf.
+ *   Q       device bf16 (rotated), rows of q_stride elements, as in hbl_kv_append
+ *   tables  device int32 [B][table_width]: the pages of each sequence in order; entries past
+ *           ceil(lens[b] / page_size) are not read. A page number out of range leaves its tokens out
+ *   lens    device int32 [B], 0 <= lens[b] <= table_width * page_size. Cache contents past a
+ *           sequence's length are not used, whatever their bits
+ *   O       device bf16 [B][Hq][D], 16-byte aligned; lse device fp32 [B][Hq] (natural log of the sum
+ *           of exp(scale q . k~)) or NULL
+ *   workspace  device scratch, ws_bytes >= hbl_attn_decode_workspace(B, Hq, Hkv, D), 256-byte aligned.
+ *           It needs no initial contents and keeps none between calls; calls that may overlap on the
+ *           GPU need one each
+ * B <= 4096; B = 0 does nothing. Grids do not depend on the lengths, so a captured call may be
+ * replayed with other lengths, tables and cache contents. Asynchronous. */
+size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D);
+
+hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, size_t cache_bytes, int num_pages,
+                           int page_size, const int32_t* tables, int table_width, const int32_t* lens, int B, int Hq,
+                           int Hkv, int D, int bits, float scale, void* workspace, size_t ws_bytes, void* O, float* lse,
+                           hbl_stream_t stream);
+
+/* Attention over packed prompts: sequence b has queries cu_q[b] .. cu_q[b+1]-1 and keys
+ * cu_k[b] .. cu_k[b+1]-1 (a cached prefix first, when there are more keys than queries).
+ *   causal  query i of nq sees keys j <= i + nk - nq of nk; 0: all keys of its sequence. A query that
+ *           sees no key gives o = 0 and lse = -inf
+ *   Q, K, V device bf16 rows as in hbl_kv_append (K rotated)
+ *   cu_q, cu_k  device int32 [B + 1], not decreasing, 0 <= cu_q <= total_q, 0 <= cu_k <= total_k.
+ *           A sequence whose borders are not so is left out and flagged (hbl_device_status). Rows
+ *           outside every sequence have no influence on a result and are not written
+ *   max_q   host bound on the longest sequence's queries (queries beyond it are left out and flagged)
+ *   O       device bf16 [total_q][Hq][D], 16-byte aligned; lse device fp32 [total_q][Hq] or NULL
+ * D 64, 128 or 256; B <= 4096; B = 0 or total_q = 0 does nothing. Weights are rounded to bf16 for the
+ * product with V, sums are held in fp32. V must be finite within a sequence. Asynchronous. */
+hbl_status hbl_attn_prompt(const void* Q, size_t q_stride, const void* K, size_t k_stride, const void* V,
+                           size_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int B, int total_q, int total_k,
+                           int max_q, int Hq, int Hkv, int D, float scale, int causal, void* O, float* lse,
+                           hbl_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * hbl_forward without a caller-provided workspace. This entry point has no counterpart in the
