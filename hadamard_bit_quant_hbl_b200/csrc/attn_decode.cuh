@@ -1,16 +1,54 @@
 // Attention of one new token per sequence over the paged low-bit cache (kv_cache.cuh):
 //
-//   s_t = scale q . k~_t,   p = softmax(s) over t < len,   o = sum_t p_t v~_t
+//   s_t = scale q . k~_t,   p = softmax(s) over t < len,   o = sum_t p_t v~_t,
+//   k~_t = gammaK_t (2 uK_t - L) / L,  v~_t = gammaV_t (2 uV_t - L) / L
 //
-// with k~, v~ the values the cached codes stand for.
+// Per cached token and KV head there are D b / 2 bits to read and 4 G D operations to do (G query
+// heads share a KV head), so the cache's bytes bound it as long as the codes reach the products
+// cheaply: at three bits a fused multiply-add per code and head would already take longer than the
+// copy. Both products therefore run on the tensor cores with the codes as fp16 operands straight
+// from a mask (kv_cache.cuh), the cache on the 16-row side and the query heads on the 8-column side:
+//
+//   S^T[t][h] = sum_d uK[t][d] q[h][d]      rows: 16 tokens, contraction: features in the order in
+//                                           which the masks deliver them, q arranged alike
+//   O^T[d][h] = sum_t uV[t][d] w[t][h]      rows: features, contraction: the same 16 tokens
+//
+// q is scaled per head by a power of two to [2^14, 2^15) and rounded to fp16 (exact for bf16 values
+// down to 2^-20 of the largest). scale gammaK (2 S - L sum q) / L gives the score; gammaV goes into
+// the weights w = p gammaV, rounded to fp16, whose largest is kept within fp16's range by running the
+// softmax's maximum over s + log2 of gammaV's binade; o = (2 O - L sum w) / (L sum p). Sums are fp32.
+// mma.sync does these products at the copy's pace (one 16x8x16 product per 256 codes) and takes A
+// from registers, where the masks leave it; tcgen05 would take 128-row tiles of shared or tensor
+// memory for at most 16 useful columns.
+//
+// gammaV's binade runs from -90 to 126 (a zero counts as -90): p is at most 2^8, so p / 2^binade stays
+// in range, and a weight that leaves fp32's range below belongs to a token whose gamma is 2^96 times
+// smaller than another's, or whose share is below 2^-30.
+//
+// Split: the (sequence, KV head, 32-token block) triples of the whole batch are laid end to end and
+// divided evenly over the CTAs, whatever the lengths; a piece of a sequence that a CTA does not hold
+// alone leaves (max, sum, o) in the workspace and attn_decode_join_kernel adds the pieces in order.
+// Inside a CTA each warp takes every fourth block of a piece through its own ring of bulk copies.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kv_cache.cuh"
 
 namespace hbl {
 
-constexpr int kDecodeMaxB = 4096;  // sequences of one call
+constexpr int kDecodeMaxB = 4096;   // sequences of one call
+constexpr int kDecodeWarps = 4;
+constexpr int kDecodeMaxCtas = 640;  // bounds the workspace
+
+// The pieces of a (sequence, column block) that begins in a CTA and ends in a later one.
+struct DecodeChain {
+  int col;    // sequence * column blocks + column block; -1: none begins here
+  int n;      // CTAs
+  int first;  // 0: it is the CTA's first piece, 1: its last
+  int pad;
+};
 
 struct DecodeAttnArgs {
   const uint16_t* Q;  // bf16; sequence b, head h at b * q_stride + h * D
@@ -18,67 +56,703 @@ struct DecodeAttnArgs {
   KvCacheView c;
   const int32_t* tables;  // [B][table_width] page numbers
   int table_width;
+  int page_shift;       // log2(page_size / 16) when that is a power of two, else -1
   const int32_t* lens;  // [B]
   int B, Hq;
-  float scale;
-  uint16_t* O;  // bf16 [B][Hq][D]
-  float* lse;   // [B][Hq] or nullptr
+  int group, groups;  // query heads per block of columns; blocks per KV head
+  float scale;        // scale * log2(e) / L
+  int min_blocks;     // per CTA
+  uint16_t* O;        // bf16 [B][Hq][D]
+  float* lse;         // [B][Hq] or nullptr
+  DecodeChain* chains;  // [CTAs]
+  float* ws;            // [CTAs][2][group][D + 2]: a CTA's first piece, then its last
 };
 
-// One warp per (sequence, query head); lane l holds features l, l + 32, ...
-template <int D, int BITS>
-__global__ void __launch_bounds__(128) attn_decode_kernel(const DecodeAttnArgs a) {
+template <int D, int BITS, int NT>
+struct DecodeCfg {
   using Rec = KvRec<D, BITS>;
-  constexpr int E = D / 32;
+  static constexpr int kChunks = Rec::kBytes <= 2560 ? 2 : 1;  // records per block of the ring
+  static constexpr int kBlock = 16 * kChunks;                  // tokens
+  static constexpr int kStageBytes = kChunks * Rec::kBytes;
+  static constexpr int kStages = kStageBytes <= 4500 ? 3 : 2;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kRow = D + 4;  // floats of a head's row in the merge scratch
+  static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
+  static constexpr int kSmem = kRing + kDecodeWarps * kHeads * kRow * 4;
+};
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held as a fragment (row lane/4, columns 2(lane%4), +1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// ---------------------------------------------------------------- codes as fp16 operands
+
+template <int BITS>
+struct HalfCodes {
+  // codes of a 16-bit half-word, and the place p of each after the shift: its fp16 value is u 2^(p-24)
+  static constexpr int kN = BITS == 3 ? 5 : 16 / BITS;
+  static constexpr int kDirect = BITS == 8 ? 1 : BITS == 4 ? 2 : BITS == 3 ? 3 : 5;  // before the shift
+  __host__ __device__ static constexpr int place(int s) { return BITS * (s < kDirect ? s : s - kDirect); }
+};
+
+// The codes of both halves of a word, one pair of fp16 operands per place.
+template <int BITS>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t* out) {
+  using H = HalfCodes<BITS>;
+  constexpr uint32_t kMask = ((1u << BITS) - 1u) * 0x00010001u;
+  const uint32_t hi = w >> (BITS * H::kDirect);
+#pragma unroll
+  for (int s = 0; s < H::kN; ++s) out[s] = (s < H::kDirect ? w : hi) & (kMask << H::place(s));
+}
+
+// Three bits: the pair of codes in the bits 15 of three words.
+__device__ __forceinline__ uint32_t spare_pair(uint32_t w0, uint32_t w1, uint32_t w2) {
+  return ((w0 >> 15) & 0x00010001u) | ((w1 >> 14) & 0x00020002u) | ((w2 >> 13) & 0x00040004u);
+}
+
+// Lane j (0..3) of a quad holds a quarter of a K row's features as D/8 pairs; pair i holds features
+// lo and hi (of the quarter, or for 64 features of three bits of the group of 32 that two lanes share)
+// at place p.
+template <int D, int BITS>
+struct KPairs {
+  static constexpr int kN = D / 8;
+  static constexpr bool kShared = BITS == 3 && D == 64;
+  __host__ __device__ static constexpr int lo(int i, bool odd = false) {
+    if (kShared) return i < 5 ? (odd ? 20 : 0) + i : odd ? (i == 7 ? 30 : 13 + i - 5) : 10 + i - 5;
+    if (BITS == 3) return 32 * (i / 16) + (i % 16 == 15 ? 30 : 10 * (i % 16 / 5) + i % 16 % 5);
+    using H = HalfCodes<BITS>;
+    return 2 * H::kN * (i / H::kN) + i % H::kN;
+  }
+  __host__ __device__ static constexpr int hi(int i, bool odd = false) {
+    if (BITS == 3) return lo(i, odd) + (lo(i, odd) % 32 == 30 ? 1 : 5);
+    return lo(i) + HalfCodes<BITS>::kN;
+  }
+  __host__ __device__ static constexpr int place(int i) {
+    if (kShared) return 3 * (i < 5 ? i % 3 : i - 5);
+    if (BITS == 3) return i % 16 == 15 ? 0 : HalfCodes<3>::place(i % 16 % 5);
+    return HalfCodes<BITS>::place(i % HalfCodes<BITS>::kN);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
+// The D/8 pairs of lane j's quarter of a K row.
+template <int D, int BITS>
+__device__ __forceinline__ void k_pairs(const uint8_t* row, int j, uint32_t (&out)[D / 8]) {
+  if constexpr (KPairs<D, BITS>::kShared) {
+    uint32_t w[3];
+    load_words<3>(row + (j >> 1) * 12, w);
+    const bool odd = j & 1;
+    uint32_t five[5];
+    code_pairs<3>(odd ? w[2] : w[0], five);
+    const uint32_t rest = odd ? ((w[1] >> 9) & 0x003f003fu) | (spare_pair(w[0], w[1], w[2]) << 6) : w[1];
+#pragma unroll
+    for (int s = 0; s < 5; ++s) out[s] = five[s];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) out[5 + s] = rest & (0x00070007u << (3 * s));
+  } else {
+    constexpr int N = D * BITS / 128;
+    uint32_t w[N];
+    load_words<N>(row + j * (D * BITS / 32), w);
+    if constexpr (BITS == 3) {
+#pragma unroll
+      for (int g = 0; g < N / 3; ++g) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) code_pairs<3>(w[3 * g + i], out + 16 * g + 5 * i);
+        out[16 * g + 15] = spare_pair(w[3 * g], w[3 * g + 1], w[3 * g + 2]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) code_pairs<BITS>(w[i], out + i * HalfCodes<BITS>::kN);
+    }
+  }
+}
+
+// The lanes with lane/4 = g hold D/8 features of V; feature number c of them is feature(g, c) at place(c).
+// The units (three bits: threes of units) go round the lane groups, so that a load touches every bank once.
+template <int D, int BITS>
+struct VCodes {
+  static constexpr int kN = D / 8;
+  static constexpr bool kShared = BITS == 3 && D == 64;
+  __host__ __device__ static constexpr int place(int c) {
+    if (kShared) return 3 * (c < 5 ? c % 3 : c - 5);
+    if (BITS == 3) return c % 16 == 15 ? 0 : HalfCodes<3>::place(c % 16 % 5);
+    return HalfCodes<BITS>::place(c % HalfCodes<BITS>::kN);
+  }
+  __host__ __device__ static constexpr int feature(int g, int c) {
+    if (kShared) return 16 * (g >> 1) + ((g & 1) ? (c < 5 ? 10 + c : c == 7 ? 15 : 3 + c) : c);
+    constexpr int kRun = BITS == 3 ? 16 : 16 / BITS;  // features of a unit, or of three
+    return (c / kRun * 8 + g) * kRun + c % kRun;
+  }
+};
+
+// Pairs of tokens (4j, 4j+1) -> a, (4j+2, 4j+3) -> b of the D/8 features of lane group g.
+template <int D, int BITS>
+__device__ __forceinline__ void v_codes(const uint8_t* v, int g, int j, uint32_t (&a)[D / 8], uint32_t (&b)[D / 8]) {
+  if constexpr (VCodes<D, BITS>::kShared) {
+    uint2 u[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) u[i] = *reinterpret_cast<const uint2*>(v + (3 * (g >> 1) + i) * 32 + j * 8);
+    const bool odd = g & 1;
+    uint32_t five[5];
+    code_pairs<3>(odd ? u[2].x : u[0].x, five);
+    uint32_t rest = odd ? ((u[1].x >> 9) & 0x003f003fu) | (spare_pair(u[0].x, u[1].x, u[2].x) << 6) : u[1].x;
+#pragma unroll
+    for (int s = 0; s < 5; ++s) a[s] = five[s];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) a[5 + s] = rest & (0x00070007u << (3 * s));
+    code_pairs<3>(odd ? u[2].y : u[0].y, five);
+    rest = odd ? ((u[1].y >> 9) & 0x003f003fu) | (spare_pair(u[0].y, u[1].y, u[2].y) << 6) : u[1].y;
+#pragma unroll
+    for (int s = 0; s < 5; ++s) b[s] = five[s];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) b[5 + s] = rest & (0x00070007u << (3 * s));
+  } else {
+    constexpr int N = D * BITS / 128;  // units of this lane group, in runs
+    constexpr int kRun = BITS == 3 ? 3 : 1;
+    uint2 u[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      u[i] = *reinterpret_cast<const uint2*>(v + (i / kRun * 8 * kRun + g * kRun + i % kRun) * 32 + j * 8);
+    if constexpr (BITS == 3) {
+#pragma unroll
+      for (int k = 0; k < N / 3; ++k) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          code_pairs<3>(u[3 * k + i].x, a + 16 * k + 5 * i);
+          code_pairs<3>(u[3 * k + i].y, b + 16 * k + 5 * i);
+        }
+        a[16 * k + 15] = spare_pair(u[3 * k].x, u[3 * k + 1].x, u[3 * k + 2].x);
+        b[16 * k + 15] = spare_pair(u[3 * k].y, u[3 * k + 1].y, u[3 * k + 2].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        code_pairs<BITS>(u[i].x, a + i * HalfCodes<BITS>::kN);
+        code_pairs<BITS>(u[i].y, b + i * HalfCodes<BITS>::kN);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the work's order
+
+__device__ __forceinline__ int decode_len(const DecodeAttnArgs& a, int b) {
+  const long long most = (long long)a.table_width * a.c.page_size;
+  const int n = a.lens[b];
+  return n < 0 ? 0 : n > most ? (int)most : n;
+}
+
+// First block of CTA i of n, of `total` blocks.
+__device__ __forceinline__ long long decode_first(long long total, int i, int n) { return total * i / n; }
+
+__device__ __forceinline__ int decode_ctas(long long total, int min_blocks, int grid) {
+  const long long want = (total + min_blocks - 1) / min_blocks;
+  return want < grid ? (int)want : grid;
+}
+
+// A piece: blocks j0 .. j1-1 of (sequence b, column block h); `rest` blocks of the CTA follow it.
+template <int BLOCK>
+struct DecodePiece {
+  int b, h, j0, j1, len;
+  long long rest;
+  __device__ __forceinline__ void cut() {
+    const int nb = (len + BLOCK - 1) / BLOCK;
+    const long long n = nb - j0;
+    j1 = rest < n ? j0 + (int)rest : nb;
+    rest -= j1 - j0;
+  }
+  // the next piece; false at the end of the CTA's blocks
+  __device__ __forceinline__ bool next(const DecodeAttnArgs& a) {
+    if (rest <= 0) return false;
+    if (++h == a.c.Hkv * a.groups) {
+      h = 0;
+      do {
+        len = decode_len(a, ++b);
+      } while (len == 0);
+    }
+    j0 = 0;
+    cut();
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const DecodeAttnArgs a) {
+  using Cfg = DecodeCfg<D, BITS, NT>;
+  using Rec = KvRec<D, BITS>;
+  using KP = KPairs<D, BITS>;
+  using VC = VCodes<D, BITS>;
+  using Piece = DecodePiece<Cfg::kBlock>;
+  constexpr int CH = Cfg::kChunks, ST = Cfg::kStages, TILES = D / 16;
   constexpr float kL = (float)((1 << BITS) - 1);
+  extern __shared__ __align__(128) uint8_t dec_smem[];
+  __shared__ __align__(8) uint64_t bars[kDecodeWarps][ST];
+  __shared__ int valid[kDecodeWarps][ST][CH];  // tokens of each chunk that count
+  __shared__ float merge_m[kDecodeWarps][Cfg::kHeads], merge_l[kDecodeWarps][Cfg::kHeads];
+  __shared__ long long scan[kDecodeWarps];
+  __shared__ int start_b;
+  __shared__ long long start_off;
+  __shared__ volatile int abort_flag;
+  float* scratch = reinterpret_cast<float*>(dec_smem + Cfg::kRing);
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, j = lane & 3;
+  const int hcols = a.c.Hkv * a.groups;  // column blocks per sequence
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    start_b = -1;
+    for (int w = 0; w < kDecodeWarps; ++w)
+      for (int s = 0; s < ST; ++s) mbar_init(&bars[w][s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long bh = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (bh >= (long long)a.B * a.Hq) return;
-  const int b = (int)(bh / a.Hq), h = (int)(bh % a.Hq), hk = h / (a.Hq / a.c.Hkv);
-  const int per_page = a.c.page_size / kKvChunk;
-  float q[E], o[E];
+
+  // the batch's blocks, and where this CTA's begin: a thread sums a run of consecutive sequences
+  const int run = (a.B + 32 * kDecodeWarps - 1) / (32 * kDecodeWarps);
+  const int b_lo = threadIdx.x * run, b_hi = b_lo + run < a.B ? b_lo + run : a.B;
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int len = decode_len(a, b);
+    if (blockIdx.x == 0 && len != a.lens[b]) raise_error(kErrBadIndex);
+    mine += (len + Cfg::kBlock - 1) / Cfg::kBlock;
+  }
+  long long upto = mine;  // inclusive scan over the threads
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)a.Q[(size_t)b * a.q_stride + (size_t)h * D + lane + 32 * e] << 16);
-    o[e] = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-  int len = a.lens[b];
-  if (len < 0 || len > (long long)a.table_width * a.c.page_size) {
-    raise_error(kErrBadIndex);
-    len = len < 0 ? 0 : a.table_width * a.c.page_size;
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    if (w < warp) upto += scan[w];
+    total += scan[w];
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < len; ++t) {
-    const int page = a.tables[(size_t)b * a.table_width + t / a.c.page_size];
-    if (page < 0 || page >= a.c.num_pages) {
-      raise_error(kErrBadIndex);
-      continue;
+  total *= hcols;
+  const int ctas = decode_ctas(total, a.min_blocks, gridDim.x);
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {  // empty sequences
+    if (decode_len(a, b) > 0) continue;
+    for (int x = threadIdx.x; x < a.Hq * D / 2; x += 32 * kDecodeWarps)
+      reinterpret_cast<uint32_t*>(a.O + (size_t)b * a.Hq * D)[x] = 0;
+    if (a.lse)
+      for (int x = threadIdx.x; x < a.Hq; x += 32 * kDecodeWarps) a.lse[(size_t)b * a.Hq + x] = -INFINITY;
+  }
+  if ((int)blockIdx.x >= ctas) {
+    if (threadIdx.x == 0) a.chains[blockIdx.x].col = -1;
+    return;
+  }
+  const long long first = decode_first(total, blockIdx.x, ctas), last = decode_first(total, blockIdx.x + 1, ctas);
+  {
+    long long at = (upto - mine) * hcols;
+    if (first >= at && first < upto * hcols) {
+      for (int b = b_lo; b < b_hi; ++b) {
+        const long long n = (long long)((decode_len(a, b) + Cfg::kBlock - 1) / Cfg::kBlock) * hcols;
+        if (first < at + n) {
+          start_b = b;
+          start_off = first - at;
+          break;
+        }
+        at += n;
+      }
     }
-    const int row = t % a.c.page_size, i = row % kKvChunk;
-    const uint8_t* rec = a.c.base + (((size_t)page * a.c.Hkv + hk) * per_page + row / kKvChunk) * (size_t)Rec::kBytes;
-    const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[i] / kL;
-    const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[i] / kL;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], 2.f * (float)kv_k_code<D, BITS>(rec, i, lane + 32 * e) - kL, s);
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= gk * a.scale;
-    const float mn = fmaxf(m, s);
-    const float f = expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(p * gv, 2.f * (float)kv_v_code<D, BITS>(rec, i, lane + 32 * e) - kL, o[e] * f);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __syncthreads();
+  if (start_b < 0) return;  // unreachable: first < total
+  Piece piece;
+  piece.b = start_b;
+  piece.len = decode_len(a, piece.b);
+  {
+    const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
+    piece.h = (int)(start_off / nb);
+    piece.j0 = (int)(start_off % nb);
+    piece.rest = last - first;
+    piece.cut();
+  }
+
+  // ---- this warp's ring of blocks, copied ahead of the products
+  uint8_t* ring = dec_smem + warp * ST * Cfg::kStageBytes;
+  Piece ahead = piece;
+  int aj = ahead.j0 + warp;
+  bool more = true;
+  int pages[CH];
+  const int per_page = a.c.page_size / kKvChunk;
+  auto settle = [&]() {  // move `ahead` to the warp's next block and read its pages' numbers
+    while (more && aj >= ahead.j1) {
+      more = ahead.next(a);
+      aj = ahead.j0 + warp;
+    }
+    if (!more) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.O[(size_t)bh * D + lane + 32 * e] = (uint16_t)(pack_bf16(o[e] * inv, 0.f) & 0xffffu);
-  if (a.lse && lane == 0) a.lse[bh] = l > 0.f ? m + logf(l) : -INFINITY;
+    for (int i = 0; i < CH; ++i) {
+      const int c = aj * CH + i;
+      if (c * kKvChunk < ahead.len)
+        pages[i] = a.tables[(size_t)ahead.b * a.table_width + (a.page_shift >= 0 ? c >> a.page_shift : c / per_page)];
+    }
+  };
+  auto copy = [&](int stage) {
+    if (!more) return;
+    if (lane == 0) {
+      const int hk = ahead.h / a.groups;
+      const uint8_t* src[CH];
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = aj * CH + i;
+        int n = ahead.len - c * kKvChunk;
+        src[i] = nullptr;
+        if (n > 0) {
+          if (pages[i] >= 0 && pages[i] < a.c.num_pages) {
+            const int in_page = a.page_shift >= 0 ? c & (per_page - 1) : c % per_page;
+            src[i] = a.c.base + (((size_t)pages[i] * a.c.Hkv + hk) * per_page + in_page) * (size_t)Rec::kBytes;
+            bytes += Rec::kBytes;
+          } else {
+            raise_error(kErrBadIndex);
+            n = 0;
+          }
+        }
+        valid[warp][stage][i] = n < 0 ? 0 : n < kKvChunk ? n : kKvChunk;
+      }
+      mbar_arrive_expect_tx(&bars[warp][stage], bytes);
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (src[i]) bulk_load_1d(ring + stage * Cfg::kStageBytes + i * Rec::kBytes, src[i], Rec::kBytes, &bars[warp][stage]);
+    }
+    aj += kDecodeWarps;
+    settle();
+  };
+  settle();
+#pragma unroll
+  for (int s = 0; s < ST; ++s) copy(s);
+
+  // fragment row r of a 16-token chunk is token 4(r/2) + r%2 for r < 8, two more for r >= 8, so that the
+  // transposed weights' pairs of tokens are those of the words v_codes loads
+  const int row0 = 4 * (g >> 1) + (g & 1);
+  RingPos pos;
+  bool first_piece = true;
+  while (true) {
+    // ---- q of this piece: fragment of the head in column g of each tile
+    const int hk = piece.h / a.groups, hg = piece.h % a.groups;
+    const int head0 = hk * (a.Hq / a.c.Hkv) + hg * a.group;
+    const int left = a.Hq / a.c.Hkv - hg * a.group;
+    const int nheads = left < a.group ? left : a.group;
+    uint32_t qf[NT][KP::kN];
+    float cA[NT][2], cB[NT][2];  // score = gammaK (cA S - cB), in powers of two, of columns 2j and 2j + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      constexpr int QN = KP::kShared ? 32 : D / 4;
+      uint32_t raw[QN / 2];
+#pragma unroll
+      for (int i = 0; i < QN / 2; ++i) raw[i] = 0;
+      if (8 * n + g < nheads) {
+        const uint16_t* qp = a.Q + (size_t)piece.b * a.q_stride + (size_t)(head0 + 8 * n + g) * D +
+                             (KP::kShared ? (j >> 1) * 32 : j * (D / 4));
+        load_words<QN / 2>(reinterpret_cast<const uint8_t*>(qp), raw);
+      }
+      auto qv = [&](int d) {
+        const uint32_t w = raw[d >> 1];
+        return __uint_as_float((d & 1) ? w & 0xffff0000u : w << 16);
+      };
+      float qmax = 0.f;
+#pragma unroll
+      for (int d = 0; d < QN; ++d) qmax = fmaxf(qmax, fabsf(qv(d)));
+      qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 1));
+      qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 2));
+      int e = (int)(__float_as_uint(qmax) >> 23) - 127;  // its binade
+      e = e < -100 ? -100 : e > 126 ? 126 : e;
+      // 2^(14 - e) may pass fp32's range, so it is applied in two steps
+      const float up0 = __uint_as_float((uint32_t)(127 + (14 - e) / 2) << 23);
+      const float up1 = __uint_as_float((uint32_t)(127 + (14 - e) - (14 - e) / 2) << 23);
+      float qsum = 0.f;
+#pragma unroll
+      for (int i = 0; i < KP::kN; ++i) {
+        float lo, hi;
+        if constexpr (KP::kShared) {
+          lo = (j & 1) ? qv(KP::lo(i, true)) : qv(KP::lo(i, false));
+          hi = (j & 1) ? qv(KP::hi(i, true)) : qv(KP::hi(i, false));
+        } else {
+          lo = qv(KP::lo(i));
+          hi = qv(KP::hi(i));
+        }
+        const __half2 r = __floats2half2_rn(lo * up0 * up1, hi * up0 * up1);
+        const float2 f = __half22float2(r);
+        qsum += f.x + f.y;
+        constexpr float one = 1.f;
+        const float down = one / (float)(1 << KP::place(i));
+        const __half2 s = __floats2half2_rn(f.x * down, f.y * down);
+        qf[n][i] = *reinterpret_cast<const uint32_t*>(&s);
+      }
+      qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+      qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+      // scale back: 2^(e - 14)
+      const float back = a.scale * __uint_as_float((uint32_t)(127 + (e - 14) / 2) << 23) *
+                         __uint_as_float((uint32_t)(127 + (e - 14) - (e - 14) / 2) << 23);
+      const float ca = back * 33554432.f, cb = back * kL * qsum;  // 2 * 2^24: a code's value is u 2^-24
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cA[n][i] = __shfl_sync(0xffffffffu, ca, 4 * (2 * j + i));
+        cB[n][i] = __shfl_sync(0xffffffffu, cb, 4 * (2 * j + i));
+      }
+    }
+
+    float acc[NT][TILES][4];
+    float m[NT][2], l[NT][2], wsum[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, l[n][i] = 0.f, wsum[n][i] = 0.f;
+    }
+
+    for (int bj = piece.j0 + warp; bj < piece.j1; bj += kDecodeWarps) {
+      if (!mbar_wait(&bars[warp][pos.s], pos.ph, &abort_flag)) more = false;  // flagged: copy nothing more
+      const uint8_t* stage = ring + pos.s * Cfg::kStageBytes;
+      float z[CH][NT][4];  // score + binade of gammaV
+      float down[CH][2], ratio[CH][2];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint8_t* rec = stage + c * Rec::kBytes;
+        const int nv = valid[warp][pos.s][c];
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+        {
+          uint32_t k0[KP::kN], k1[KP::kN];
+          k_pairs<D, BITS>(rec + row0 * Rec::kRow, j, k0);
+          k_pairs<D, BITS>(rec + (row0 + 2) * Rec::kRow, j, k1);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16_16816(s[n], k0[2 * t], k1[2 * t], k0[2 * t + 1], k1[2 * t + 1], qf[n][2 * t], qf[n][2 * t + 1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = row0 + 2 * r;
+          const bool in = row < nv;
+          const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[row];
+          const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[row];
+          int e = (int)((__float_as_uint(gv) >> 23) & 0xffu) - 127;
+          e = e < -90 ? -90 : e > 126 ? 126 : e;
+          down[c][r] = __uint_as_float((uint32_t)(127 - e) << 23);
+          ratio[c][r] = in ? gv * down[c][r] : 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              z[c][n][2 * r + i] = in ? fmaf(gk, fmaf(cA[n][i], s[n][2 * r + i], -cB[n][i]), (float)e) : -INFINITY;
+        }
+      }
+      // the running maximum moves only when a weight would pass 2^8 (fp16 holds up to 2^16)
+      bool grow = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < CH; ++c) grow |= fmaxf(z[c][n][i], z[c][n][2 + i]) > m[n][i] + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = m[n][i];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) top = fmaxf(top, fmaxf(z[c][n][i], z[c][n][2 + i]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float f = top == -INFINITY ? 1.f : ex2_approx(m[n][i] - top);
+            m[n][i] = top;
+            l[n][i] *= f;
+            wsum[n][i] *= f;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+              acc[n][t][i] *= f;
+              acc[n][t][2 + i] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        uint32_t wb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p = ex2_approx(z[c][n][2 * r + i] - (m[n][i] == -INFINITY ? 0.f : m[n][i]));
+              l[n][i] = fmaf(p, down[c][r], l[n][i]);
+              w[i] = p * ratio[c][r];
+            }
+            const __half2 h2 = __floats2half2_rn(w[0], w[1]);
+            const float2 f = __half22float2(h2);
+            wsum[n][0] += f.x;
+            wsum[n][1] += f.y;
+            wb[n][r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h2));
+          }
+        uint32_t va[VC::kN], vb[VC::kN];
+        v_codes<D, BITS>(stage + c * Rec::kBytes + Rec::kV, g, j, va, vb);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_f16_16816(acc[n][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], wb[n][0], wb[n][1]);
+      }
+      __syncwarp();  // every lane is done with the stage
+      copy(pos.s);
+      pos.advance(1, ST);
+    }
+
+    // ---- join the warps: o, sum and maximum of each head
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
+          wsum[n][i] += __shfl_xor_sync(0xffffffffu, wsum[n][i], o);
+        }
+        const int col = 8 * n + 2 * j + i;
+        float* row = scratch + (warp * Cfg::kHeads + col) * Cfg::kRow;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int c = 2 * t + r;
+            const float up = 33554432.f / (kL * (float)(1 << VC::place(c)));
+            row[c * 8 + g] = fmaf(acc[n][t][2 * r + i], up, -wsum[n][i]);
+          }
+        if (g == 0) {
+          merge_m[warp][col] = m[n][i];
+          merge_l[warp][col] = l[n][i];
+        }
+      }
+    __syncthreads();
+    const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
+    const bool whole = piece.j0 == 0 && piece.j1 == nb;
+    float* slot = a.ws + (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * a.group * (D + 2);
+    for (int x = threadIdx.x; x < nheads * D; x += 32 * kDecodeWarps) {
+      const int col = x / D, y = x % D;
+      float top = merge_m[0][col];
+#pragma unroll
+      for (int w = 1; w < kDecodeWarps; ++w) top = fmaxf(top, merge_m[w][col]);
+      float o = 0.f, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        if (merge_m[w][col] == -INFINITY) continue;  // a warp without a token in this piece
+        const float f = ex2_approx(merge_m[w][col] - top);
+        o = fmaf(f, scratch[(w * Cfg::kHeads + col) * Cfg::kRow + y], o);
+        sum = fmaf(f, merge_l[w][col], sum);
+      }
+      const int d = VC::feature(y & 7, y >> 3);
+      if (whole) {
+        const size_t bh = (size_t)piece.b * a.Hq + head0 + col;
+        a.O[bh * D + d] = (uint16_t)(pack_bf16(sum > 0.f ? o / sum : 0.f, 0.f) & 0xffffu);
+        if (y == 0 && a.lse) a.lse[bh] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        slot[col * D + d] = o;
+        if (y == 0) {
+          slot[a.group * D + col] = top;
+          slot[a.group * D + a.group + col] = sum;
+        }
+      }
+    }
+    const DecodePiece<Cfg::kBlock> done = piece;
+    if (!piece.next(a)) {
+      if (threadIdx.x == 0) {
+        DecodeChain ch = {-1, 0, first_piece ? 0 : 1, 0};
+        if (done.j0 == 0 && done.j1 < nb) {
+          const long long end = last + nb - done.j1;  // of its blocks
+          int i1 = (int)((end - 1) * ctas / total);   // the last CTA whose first block is below it
+          while (i1 + 1 < ctas && decode_first(total, i1 + 1, ctas) < end) ++i1;
+          while (decode_first(total, i1, ctas) >= end) --i1;
+          ch.col = done.b * hcols + done.h;
+          ch.n = i1 - (int)blockIdx.x + 1;
+        }
+        a.chains[blockIdx.x] = ch;
+      }
+      break;
+    }
+    first_piece = false;
+    __syncthreads();  // before the scratch is written again
+  }
+}
+
+// The pieces of the chain that begins in the main kernel's CTA blockIdx.x, added in order. A CTA for
+// each head of the column block, a thread per feature.
+static __global__ void attn_decode_join_kernel(const DecodeAttnArgs a, int D) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const DecodeChain ch = a.chains[blockIdx.x];
+  if (ch.col < 0) return;
+  const int G = a.Hq / a.c.Hkv, hcols = a.c.Hkv * a.groups;
+  const int b = ch.col / hcols, h = ch.col % hcols;
+  const int col = blockIdx.y, in_kv = h % a.groups * a.group + col;
+  if (in_kv >= G) return;
+  const size_t slot = (size_t)a.group * (D + 2);
+  const float* w0 = a.ws + 2 * blockIdx.x * slot;
+  auto place = [&](int i) { return w0 + (2 * i + (i == 0 ? ch.first : 0)) * slot; };
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < ch.n; ++i) top = fmaxf(top, place(i)[a.group * D + col]);
+  float o = 0.f, sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < ch.n; ++i) {
+    const float* p = place(i);
+    const float mi = p[a.group * D + col];
+    const float f = mi == -INFINITY ? 0.f : ex2_approx(mi - top);
+    o = fmaf(f, p[col * D + threadIdx.x], o);
+    sum = fmaf(f, p[a.group * D + a.group + col], sum);
+  }
+  const size_t bh = (size_t)b * a.Hq + h / a.groups * G + in_kv;
+  a.O[bh * D + threadIdx.x] = (uint16_t)(pack_bf16(sum > 0.f ? o / sum : 0.f, 0.f) & 0xffffu);
+  if (threadIdx.x == 0 && a.lse) a.lse[bh] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace hbl

@@ -65,6 +65,33 @@ KvCacheView view(const void* cache, int num_pages, int page_size, int Hkv) {
   return KvCacheView{static_cast<uint8_t*>(const_cast<void*>(cache)), num_pages, page_size, Hkv};
 }
 
+// Query heads that one pass over a KV head takes: up to 16 columns, 8 for 256 features (whose
+// accumulators take as many registers); more heads in equal passes.
+int decode_group(int G, int D) {
+  const int most = D == 256 ? 8 : 16;
+  const int passes = (G + most - 1) / most;
+  return (G + passes - 1) / passes;
+}
+
+template <int D, int BITS, int NT>
+hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
+  using Cfg = DecodeCfg<D, BITS, NT>;
+  static SmemLimit lim;
+  auto* k = attn_decode_kernel<D, BITS, NT>;
+  const cudaError_t e = allow_smem(k, Cfg::kSmem, lim);
+  if (e != cudaSuccess) return cuda_fail(e);
+  // every CTA resident at once, and no more than the tables have room for
+  const long long blocks = ((long long)a.table_width * a.c.page_size + Cfg::kBlock - 1) / Cfg::kBlock;
+  a.min_blocks = kDecodeWarps;
+  const long long want = (blocks * a.B * a.c.Hkv * a.groups + a.min_blocks - 1) / a.min_blocks;
+  int grid = resident_ctas(k, 32 * kDecodeWarps, Cfg::kSmem, lim);
+  if (grid > kDecodeMaxCtas) grid = kDecodeMaxCtas;
+  if (want < grid) grid = (int)want;
+  const hbl_status st = launch_pdl(k, dim3(grid), dim3(32 * kDecodeWarps), Cfg::kSmem, s, a);
+  if (st != HBL_OK) return st;
+  return launch_pdl(attn_decode_join_kernel, dim3(grid, a.group), dim3(D), 0, s, a, D);
+}
+
 }  // namespace
 
 extern "C" {
@@ -142,8 +169,8 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
 }
 
 size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-  return 256;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
+  return round_up(kDecodeMaxCtas * (sizeof(DecodeChain) + (size_t)2 * decode_group(Hq / Hkv, D) * (D + 2) * sizeof(float)), 256);
 }
 
 hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, size_t cache_bytes, int num_pages,
@@ -153,7 +180,7 @@ hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, si
   const hbl_status st = check_cache(cache, cache_bytes, num_pages, page_size, Hkv, D, bits);
   if (st != HBL_OK) return st;
   if (B < 0 || Hq < 1 || Hq % Hkv != 0 || table_width < 1 || !isfinite(scale)) return HBL_EINVAL;
-  if (B > kDecodeMaxB || (long long)table_width * page_size > 0x7fffffffll) return HBL_EUNSUPPORTED;
+  if (B > kDecodeMaxB || Hq > 65535 || (long long)table_width * page_size > 0x7fffffffll) return HBL_EUNSUPPORTED;
   if (B == 0) return HBL_OK;
   if (!rows_ok(Q, q_stride, Hq, D) || !tables || !aligned(tables, 4) || !lens || !aligned(lens, 4)) return HBL_EINVAL;
   if (!O || !aligned(O, 16) || (lse && !aligned(lse, 4))) return HBL_EINVAL;
@@ -167,12 +194,22 @@ hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, si
   a.lens = lens;
   a.B = B;
   a.Hq = Hq;
-  a.scale = scale;
+  const int G = Hq / Hkv;
+  a.group = decode_group(G, D);
+  a.groups = (G + a.group - 1) / a.group;
+  const int per_page = page_size / kKvChunk;
+  a.page_shift = is_pow2(per_page) ? ilog2_c(per_page) : -1;
+  a.scale = scale * 1.44269504088896340736f / (float)((1 << bits) - 1);
   a.O = static_cast<uint16_t*>(O);
   a.lse = lse;
+  a.chains = static_cast<DecodeChain*>(workspace);
+  a.ws = reinterpret_cast<float*>(a.chains + kDecodeMaxCtas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return for_head(D, bits, [&](auto d, auto b) {
-    return launch_pdl(attn_decode_kernel<d(), b()>, dim3((unsigned)(((long long)B * Hq + 3) / 4)), dim3(128), 0, s, a);
+    if constexpr (d() <= 128) {
+      if (a.group > 8) return launch_decode_attn<d(), b(), 2>(a, s);
+    }
+    return launch_decode_attn<d(), b(), 1>(a, s);
   });
 }
 

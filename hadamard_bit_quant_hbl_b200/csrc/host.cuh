@@ -48,6 +48,7 @@ inline int device_sms(int dev) {
 struct SmemLimit {
   std::mutex mu;
   int allowed[64] = {0};
+  int resident[64] = {0};  // CTAs of the kernel that fit on the device at once (see resident_ctas)
 };
 
 template <typename F>
@@ -65,6 +66,23 @@ cudaError_t allow_smem(F* kernel, int bytes, SmemLimit& lim) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess) lim.allowed[dev] = bytes;
   return e;
+}
+
+// CTAs of a kernel that fit on the current device at once, for launches that always take the same
+// threads and shared memory.
+template <typename F>
+int resident_ctas(F* kernel, int threads, int smem, SmemLimit& lim) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(lim.mu);
+  int& n = lim.resident[dev & 63];
+  if (n == 0) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+      per_sm = 1;
+    n = per_sm * device_sms(dev);
+  }
+  return n;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
