@@ -2,9 +2,40 @@
 //
 //   query i of a sequence with nq queries and nk keys sees keys j <= i + nk - nq (causal) or all,
 //   p = softmax(scale q . k),   o = sum_j p_j v_j
+//
+// 4 D operations per visible (query, key) pair against 2 D bytes of a key for all the queries of a tile:
+// bound by the tensor cores and, next to them, by one exp per pair (16 a clock and SM, so that a
+// 128 x 128 tile of 128 features takes both of them about 1024 clocks).
+//
+// A tile is 128 rows of (token, query head), heads of one KV head packed together as far as a power of
+// two divides their number, so that few tokens fill it too. A CTA holds two tiles of neighbouring tokens
+// (one for 256 features, whose accumulator takes half of tensor memory) and passes the key blocks once:
+//
+//   S = Q K^T      tcgen05.mma, both operands in shared memory, 128 columns of tensor memory
+//   P = exp2(scale log2(e) (S - m)), rounded to bf16 over the same columns; sums in fp32 before rounding
+//   O += P V       tcgen05.mma, P from tensor memory, V as it lies (its features contiguous)
+//
+// The running maximum m moves only when a row's scores pass it by more than 8 binades of the weights
+// (they stay below 2^8), so O is rarely rescaled, by the softmax threads themselves. A thread holds a
+// row, so its statistics need no exchange.
+//
+//   warps 0-3 (4-7)  softmax of the first (second) tile, then its output
+//   next warp        issues the products: while one tile is in its softmax, the other's P V and the next
+//                    S run. Rows of V behind a sequence's last key, which may hold anything, are
+//                    cleared in shared memory (the scores of such keys are replaced by -inf)
+//   last warp        TMA copies of Q, then of K and V blocks through a ring
+//
+// One CTA per SM; a launch has a CTA per (tile pair, head group), the pairs of most keys first. Sizes of
+// sequences are read on the device: a CTA finds its tile from the borders.
 #pragma once
 
+#include <cuda.h>
+
+#include <type_traits>
+
 #include "common.cuh"
+#include "gemm_swap.cuh"
+#include "gemm_tc.cuh"
 #include "kv_cache.cuh"
 
 namespace hbl {
@@ -16,8 +47,10 @@ struct PromptAttnArgs {
   size_t q_stride, k_stride, v_stride;
   const int32_t *cu_q, *cu_k;  // [B + 1]
   int B, total_q, total_k, max_q, Hq, Hkv;
-  float scale;
+  float scale_log2;  // |scale| log2(e), 1 for a zero scale
+  float sign;        // of the scale, 0 for a zero scale
   int causal;
+  int pack, groups;  // query heads packed into a tile; such groups per KV head
   uint16_t* O;  // bf16 [total_q][Hq][D]
   float* lse;   // [total_q][Hq] or nullptr
 };
@@ -32,77 +65,449 @@ __device__ __forceinline__ bool prompt_borders(const PromptAttnArgs& a, int b, i
   return q0 >= 0 && q0 <= q1 && q1 <= a.total_q && k0 >= 0 && k0 <= k1 && k1 <= a.total_k;
 }
 
-// One warp per (query, head); a lane holds a key's score, then lane l features l, l + 32, ... of V.
 template <int D>
-__global__ void __launch_bounds__(128) attn_prompt_kernel(const PromptAttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float qs[4][D];
+struct PromptCfg {
+  static constexpr int kTiles = D == 256 ? 1 : 2;
+  static constexpr int kKeys = D == 256 ? 64 : 128;  // of a block
+  static constexpr int kChunks = D / 64;             // 128-byte columns of a row
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kStageBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kThreads = 32 * (kSoftWarps + 2);
+  // tensor memory: two buffers of scores, then the accumulators
+  static constexpr int kScores = 128;  // columns between the buffers
+  static constexpr int kAcc = 256;
+};
+
+__host__ __device__ constexpr uint32_t prompt_idesc(int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// V block: features contiguous, 64 of them to a 128-byte swizzled row, keys one row after the other;
+// chunks of 64 features lie chunk_bytes apart, groups of eight keys 1024 bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3fffu);
+  d |= (uint64_t)((chunk_bytes >> 4) & 0x3fffu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// 32 columns of this thread's lane, not waited for; tmem_ld_wait ties the registers to the wait.
+__device__ __forceinline__ void tmem_ld_nowait_x32(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
+        "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]),
+        "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]),
+        "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+}
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
+attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                   const __grid_constant__ CUtensorMap mapV, const PromptAttnArgs a) {
+  using Cfg = PromptCfg<D>;
+  constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages, THREADS = Cfg::kThreads;
+  constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + 1;
+  extern __shared__ __align__(1024) uint8_t prompt_smem[];
+  __shared__ __align__(8) uint64_t q_full, kv_full[ST], kv_empty[ST], s_full[2], p_full[2], o_done[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ int scan[THREADS / 32], found[2];  // sequence, tile pair within it
+
+  uint8_t* smem = align_shared<1024>(prompt_smem);
+  uint8_t* ring = smem + NT * Cfg::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hx = a.Hkv * a.groups;  // head groups
+  const int tile = blockIdx.x / hx, hq = blockIdx.x % hx;
+  const int per_tile = 128 / a.pack;  // tokens of a tile
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    found[0] = -1;
+    mbar_init(&q_full, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);  // the warps of a tile
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(&drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&mapQ);
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x * 4 + warp, h = blockIdx.y, hk = h / (a.Hq / a.Hkv);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-      int nq, nk, q0, k0;
-      if (!prompt_borders(a, b, q0, nq, k0, nk) || nq > a.max_q) raise_error(kErrBadIndex);
+
+  // ---- which tile pair: a thread counts those of a run of consecutive sequences
+  {
+    const int run = (a.B + THREADS - 1) / THREADS;
+    const int b_lo = threadIdx.x * run, b_hi = b_lo + run < a.B ? b_lo + run : a.B;
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      int q0, nq, k0, nk;
+      const bool good = prompt_borders(a, b, q0, nq, k0, nk);
+      if (blockIdx.x == 0 && (!good || nq > a.max_q)) raise_error(kErrBadIndex);
+      if (good) mine += ((nq < a.max_q ? nq : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
     }
-  if (i >= a.total_q) return;
-  int lo = 0, hi = a.B;  // the sequence: the last b with cu_q[b] <= i
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= i) lo = mid; else hi = mid;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w)
+      if (w < warp) upto += scan[w];
+    int at = upto - mine;
+    if (tile >= at && tile < upto) {
+      for (int b = b_lo; b < b_hi; ++b) {
+        int q0, nq, k0, nk;
+        if (!prompt_borders(a, b, q0, nq, k0, nk)) continue;
+        const int n = ((nq < a.max_q ? nq : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
+        if (tile < at + n) {
+          found[0] = b;
+          found[1] = n - 1 - (tile - at);  // the last tokens see most keys
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
   }
-  int q0, nq, k0, nk;
-  if (!prompt_borders(a, lo, q0, nq, k0, nk) || i < q0 || i >= q0 + nq || i - q0 >= a.max_q) return;
-  int seen = a.causal ? i - q0 + 1 + nk - nq : nk;
-  seen = seen < 0 ? 0 : seen > nk ? nk : seen;
-  for (int d = lane; d < D; d += 32)
-    qs[warp][d] = __uint_as_float((uint32_t)a.Q[(size_t)i * a.q_stride + (size_t)h * D + d] << 16);
-  __syncwarp();
-  float o[E], m = -INFINITY, l = 0.f;
+  const int b = found[0];
+  if (b < 0) return;  // fewer tiles than the grid has room for
+  int q0, nq_all, k0, nk;
+  prompt_borders(a, b, q0, nq_all, k0, nk);
+  const int nq = nq_all < a.max_q ? nq_all : a.max_q;
+  const int first = found[1] * NT * per_tile;  // token of the sequence
+  const int hk = hq / a.groups, head0 = hk * (a.Hq / a.Hkv) + hq % a.groups * a.pack;
+  auto seen = [&](int token) {
+    const int n = a.causal ? token + 1 + nk - nq_all : nk;
+    return n < 0 ? 0 : n > nk ? nk : n;
+  };
+  int blocks[NT], most = 0;  // key blocks that a tile sees
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int j0 = 0; j0 < seen; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    if (j < seen) {
-      const uint4* k = reinterpret_cast<const uint4*>(a.K + (size_t)(k0 + j) * a.k_stride + (size_t)hk * D);
-      s = 0.f;
-      for (int d = 0; d < D; d += 8) {
-        const uint4 u = k[d / 8];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int t = 0; t < NT; ++t) {
+    const int lo = first + t * per_tile, hi = lo + per_tile < nq ? lo + per_tile : nq;
+    blocks[t] = lo < nq ? (seen(hi - 1) + BN - 1) / BN : 0;
+    most = blocks[t] > most ? blocks[t] : most;
+  }
+
+  if (warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == TMA_WARP) {
+    if (lane == 0 && most > 0) {
+      uint32_t bytes = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s = fmaf(qs[warp][d + 2 * e], __uint_as_float(w[e] << 16), s);
-          s = fmaf(qs[warp][d + 2 * e + 1], __uint_as_float(w[e] & 0xffff0000u), s);
+      for (int t = 0; t < NT; ++t) bytes += blocks[t] > 0 ? Cfg::kQBytes : 0;
+      mbar_arrive_expect_tx(&q_full, bytes);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (blocks[t] > 0)
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full, 64 * c, head0,
+                        q0 + first + t * per_tile);
+      RingPos pos;
+      int issued = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int j) {
+        if (ok) ok = mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&kv_full[pos.s], Cfg::kStageBytes);
+        for (int c = 0; c < Cfg::kChunks; ++c)
+          tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, &kv_full[pos.s], 64 * c, hk, k0 + j * BN);
+        pos.advance(1, ST);
+        ++issued;
+      };
+      // in the order of the products below
+      load(&mapK, 0);
+      for (int j = 0; j < most; ++j) {
+        if (NT == 1) {
+          if (j + 1 < most) load(&mapK, j + 1);
+          load(&mapV, j);
+        } else {
+          load(&mapV, j);
+          if (j + 1 < most) load(&mapK, j + 1);
         }
       }
-      s *= a.scale;
+      if (abort_flag) {  // no copy may still be landing when the CTA exits
+        drain_wait(&q_full, 0);
+        for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
+      }
     }
-    float mx = s;
+  } else if (warp == MMA_WARP) {
+    if (most > 0) {
+      constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
+      bool ok = mbar_wait(&q_full, 0, &abort_flag);
+      RingPos pos;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+        tc_fence_after();
+      };
+      // scores of the tile in shared memory q against the K block in stage s
+      auto scores = [&](int q, int s, int buf) {
+        if (lane != 0 || !ok) return;
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + q * Cfg::kQBytes));
+        const uint64_t kd = smem_desc_sw128(smem_u32(ring + s * Cfg::kStageBytes));
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    const float mn = fmaxf(m, mx);
-    const float f = expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16_ss(tmem + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
+                      kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
+        mma_commit(&s_full[buf]);
+      };
+      auto weigh = [&](int t, int s, int buf, bool acc) {
+        if (lane != 0 || !ok) return;
+        const uint64_t vd = smem_desc_sw128_mn(smem_u32(ring + s * Cfg::kStageBytes), BN * 128);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= f;
-    const int n = seen - j0 < 32 ? seen - j0 : 32;
-    for (int t = 0; t < n; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, p, t);
-      const uint16_t* v = a.V + (size_t)(k0 + j0 + t) * a.v_stride + (size_t)hk * D;
+        for (int k = 0; k < BN / 16; ++k)
+          mma_bf16_ts(tmem + Cfg::kAcc + t * D, tmem + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o,
+                      acc || k > 0);
+        mma_commit(&o_done[t]);
+      };
+      auto release = [&](int s) {
+        if (lane == 0 && ok) mma_commit(&kv_empty[s]);
+      };
+      // waits for the V block j in the ring's next stage and clears its rows behind the last key
+      auto take_v = [&](int j) {
+        wait(&kv_full[pos.s], pos.ph);
+        if (ok && (j + 1) * BN > nk) {
+          const int keep = nk - j * BN;
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            for (int x = keep * 8 + lane; x < BN * 8; x += 32)
+              reinterpret_cast<uint4*>(ring + pos.s * Cfg::kStageBytes + c * (BN * 128))[x] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_shared();
+          __syncwarp();
+        }
+      };
+      wait(&kv_full[pos.s], pos.ph);
+      if constexpr (NT == 2) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(pt, __uint_as_float((uint32_t)v[lane + 32 * e] << 16), o[e]);
+        for (int t = 0; t < NT; ++t)
+          if (blocks[t] > 0) scores(t, pos.s, t);
+        release(pos.s);
+        pos.advance(1, ST);
+        for (int j = 0; j < most && ok; ++j) {
+          take_v(j);
+          const int vs = pos.s;
+          pos.advance(1, ST);
+          const bool next = j + 1 < most;
+          if (next) wait(&kv_full[pos.s], pos.ph);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (j < blocks[t]) {
+              wait(&p_full[t], (uint32_t)j & 1u);
+              weigh(t, vs, t, j > 0);
+            }
+            if (t == NT - 1) release(vs);
+            if (j + 1 < blocks[t]) scores(t, pos.s, t);
+          }
+          if (next) {
+            release(pos.s);
+            pos.advance(1, ST);
+          }
+        }
+      } else {
+        scores(0, pos.s, 0);
+        release(pos.s);
+        pos.advance(1, ST);
+        for (int j = 0; j < most && ok; ++j) {
+          if (j + 1 < most) {
+            wait(&kv_full[pos.s], pos.ph);
+            scores(0, pos.s, (j + 1) & 1);
+            release(pos.s);
+            pos.advance(1, ST);
+          }
+          take_v(j);
+          wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
+          weigh(0, pos.s, j & 1, j > 0);
+          release(pos.s);
+          pos.advance(1, ST);
+        }
+      }
+      if (!ok && lane == 0) {  // no product may still be running when the CTA exits
+        mma_commit(&drain);
+        drain_wait(&drain, 0);
+      }
+    }
+  } else {
+    // ---- softmax: a thread per row
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_acc = tmem + lanes + Cfg::kAcc + t * D;
+    const int token = first + t * per_tile + row / a.pack, head = head0 + row % a.pack;
+    const int n = blocks[NT == 1 ? 0 : t];
+    const int visible = seen(token);
+    const int unmasked = seen(first + t * per_tile);  // keys that every row of the tile sees
+    const float sl2 = a.scale_log2;
+    const float slack = 8.f / sl2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int buf = NT == 1 ? j & 1 : t;
+      ok = mbar_wait(&s_full[buf], (uint32_t)(NT == 1 ? j >> 1 : j) & 1u, &abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = tmem + lanes + buf * Cfg::kScores;
+      float s[BN];
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) tmem_ld_nowait_x32(t_s + c, s + c);
+      tmem_ld_wait(s);
+      if (a.sign != 1.f) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c) s[c] *= a.sign;
+      }
+      if ((j + 1) * BN > unmasked) {
+        const int lim = visible - j * BN;
+#pragma unroll
+        for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < BN; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = c + 4 + i < BN ? fmaxf(fmaxf(mx[i], s[c + i]), s[c + 4 + i]) : fmaxf(mx[i], s[c + i]);
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool up = top > m + slack;
+      if (j == 0) {
+        m = top;
+      } else if (__any_sync(0xffffffffu, up)) {
+        const float mn = up ? top : m;
+        const float f = up ? ex2_fast((m - mn) * sl2) : 1.f;
+        m = mn;
+        l *= f;
+        if (NT == 1) {  // with two tiles the products before these scores are known to be complete
+          ok = mbar_wait(&o_done[0], (uint32_t)(j - 1) & 1u, &abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld_nowait_x32(t_acc + c, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f;
+          tmem_st_32x32b_x32(t_acc + c, reinterpret_cast<const uint32_t(&)[32]>(o));
+        }
+      }
+      const float shift = m == -INFINITY ? 0.f : -m * sl2;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < BN; c += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float p0 = ex2_fast(fmaf(s[c + 2 * i], sl2, shift)), p1 = ex2_fast(fmaf(s[c + 2 * i + 1], sl2, shift));
+          sum[2 * (i & 1)] += p0;
+          sum[2 * (i & 1) + 1] += p1;
+          p[i] = pack_bf16(p0, p1);
+        }
+        tmem_st_32x32b_x32(t_s + c / 2, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[buf]);
+    }
+    if (ok && n > 0) {
+      // one phase at a time: with one tile the last scores only tell that the products of block n - 3 are done
+      if (NT == 1 && n > 1) mbar_wait(&o_done[t], (uint32_t)(n - 2) & 1u, &abort_flag);
+      ok = mbar_wait(&o_done[t], (uint32_t)(n - 1) & 1u, &abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const bool store = ok && token < nq;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t ih = (size_t)(q0 + token) * a.Hq + head;
+    if (store && a.lse) a.lse[ih] = l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld_nowait_x32(t_acc + c, o);
+          tmem_ld_wait(o);
+        }
+        if (store) {
+          uint4* dst = reinterpret_cast<uint4*>(a.O + ih * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = inv > 0.f ? pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
     }
   }
-#pragma unroll
-  for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t ih = (size_t)i * a.Hq + h;
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.O[ih * D + lane + 32 * e] = (uint16_t)(pack_bf16(o[e] * inv, 0.f) & 0xffffu);
-  if (a.lse && lane == 0) a.lse[ih] = l > 0.f ? m + logf(l) : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
 }
 
 }  // namespace hbl

@@ -92,6 +92,47 @@ hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   return launch_pdl(attn_decode_join_kernel, dim3(grid, a.group), dim3(D), 0, s, a, D);
 }
 
+// bf16 states [T][H][D] with rows `stride` elements apart, in boxes of 64 features, `heads` heads and
+// `tokens` tokens, laid out in 128-byte swizzled rows.
+bool make_map_rows(CUtensorMap* map, const void* base, size_t stride, int T, int H, int D, int heads, int tokens) {
+  auto enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2u, (cuuint64_t)stride * 2u};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)heads, (cuuint32_t)tokens};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+template <int D>
+hbl_status launch_prompt(const PromptAttnArgs& a, cudaStream_t s) {
+  using Cfg = PromptCfg<D>;
+  static SmemLimit lim;
+  auto* k = attn_prompt_kernel<D>;
+  const cudaError_t e = allow_smem(k, Cfg::kSmem, lim);
+  if (e != cudaSuccess) return cuda_fail(e);
+  CUtensorMap mq, mk, mv;
+  if (!make_map_rows(&mq, a.Q, a.q_stride, a.total_q, a.Hq, D, a.pack, 128 / a.pack)) return HBL_ECUDA;
+  if (a.total_k > 0) {
+    if (!make_map_rows(&mk, a.K, a.k_stride, a.total_k, a.Hkv, D, 1, Cfg::kKeys)) return HBL_ECUDA;
+    if (!make_map_rows(&mv, a.V, a.v_stride, a.total_k, a.Hkv, D, 1, Cfg::kKeys)) return HBL_ECUDA;
+  } else {
+    mk = mv = mq;  // never read: there is no key block
+  }
+  // as many tile pairs as the borders could ask for, whatever they are
+  const long long tokens = (long long)Cfg::kTiles * 128 / a.pack;
+  long long tiles = a.total_q / tokens + a.B;
+  const long long bound = (long long)a.B * ((a.max_q + tokens - 1) / tokens);
+  if (bound < tiles) tiles = bound;
+  const long long grid = tiles * a.Hkv * a.groups;
+  if (grid == 0) return HBL_OK;
+  if (grid > 0x7fffffffll) return HBL_EUNSUPPORTED;
+  return launch_pdl(k, dim3((unsigned)grid), dim3(Cfg::kThreads), Cfg::kSmem, s, mq, mk, mv, a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -240,15 +281,19 @@ hbl_status hbl_attn_prompt(const void* Q, size_t q_stride, const void* K, size_t
   a.max_q = max_q;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.scale = scale;
+  a.scale_log2 = scale == 0.f ? 1.f : fabsf(scale) * 1.44269504088896340736f;
+  a.sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+  const int G = Hq / Hkv;
+  a.pack = G & -G;  // the largest power of two that divides it
+  if (a.pack > 128) a.pack = 128;
+  a.groups = G / a.pack;
   a.causal = causal != 0;
   a.O = static_cast<uint16_t*>(O);
   a.lse = lse;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((total_q + 3) / 4, Hq);
-  if (D == 64) return launch_pdl(attn_prompt_kernel<64>, grid, dim3(128), 0, s, a);
-  if (D == 128) return launch_pdl(attn_prompt_kernel<128>, grid, dim3(128), 0, s, a);
-  return launch_pdl(attn_prompt_kernel<256>, grid, dim3(128), 0, s, a);
+  if (D == 64) return launch_prompt<64>(a, s);
+  if (D == 128) return launch_prompt<128>(a, s);
+  return launch_prompt<256>(a, s);
 }
 
 }  // extern "C"
