@@ -25,7 +25,12 @@
 // in range, and a weight that leaves fp32's range below belongs to a token whose gamma is 2^96 times
 // smaller than another's, or whose share is below 2^-30.
 //
-// Split: the (sequence, KV head, 32-token block) triples of the whole batch are laid end to end and
+// Up to four query heads to a KV head fill less than half of the eight columns. There q is repeated in
+// two or four groups of columns, and a lane keeps the scores of the chunk that its columns' group stands
+// for: one softmax pass then serves two or four chunks of 16 tokens. The weights' other groups are
+// zeroed for the product with a chunk's V, and the groups are joined like the pieces of the warps.
+//
+// Split: the (sequence, KV head, 64-token block) triples of the whole batch are laid end to end and
 // divided evenly over the CTAs, whatever the lengths; a piece of a sequence that a CTA does not hold
 // alone leaves (max, sum, o) in the workspace and attn_decode_join_kernel adds the pieces in order.
 // Inside a CTA each warp takes every fourth block of a piece through its own ring of bulk copies.
@@ -65,16 +70,17 @@ struct DecodeAttnArgs {
   uint16_t* O;        // bf16 [B][Hq][D]
   float* lse;         // [B][Hq] or nullptr
   DecodeChain* chains;  // [CTAs]
-  float* ws;            // [CTAs][2][group][D + 2]: a CTA's first piece, then its last
+  float* ws;            // [CTAs][2][group][D + 4]: a CTA's first piece, then its last
 };
 
 template <int D, int BITS, int NT>
 struct DecodeCfg {
   using Rec = KvRec<D, BITS>;
-  static constexpr int kChunks = Rec::kBytes <= 2560 ? 2 : 1;  // records per block of the ring
-  static constexpr int kBlock = 16 * kChunks;                  // tokens
+  // records per block of the ring: the warps' two stages within about 70 KB
+  static constexpr int kChunks = Rec::kBytes <= 2304 ? 4 : Rec::kBytes <= 4608 ? 2 : 1;
+  static constexpr int kBlock = 16 * kChunks;  // tokens
   static constexpr int kStageBytes = kChunks * Rec::kBytes;
-  static constexpr int kStages = kStageBytes <= 4500 ? 3 : 2;
+  static constexpr int kStages = 2;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRow = D + 4;  // floats of a head's row in the merge scratch
   static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
@@ -311,7 +317,8 @@ struct DecodePiece {
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D, int BITS, int NT>
+// R groups of 8 / R columns, each for another chunk (R = 1 where NT = 2).
+template <int D, int BITS, int NT, int R>
 __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const DecodeAttnArgs a) {
   using Cfg = DecodeCfg<D, BITS, NT>;
   using Rec = KvRec<D, BITS>;
@@ -319,6 +326,9 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
   using VC = VCodes<D, BITS>;
   using Piece = DecodePiece<Cfg::kBlock>;
   constexpr int CH = Cfg::kChunks, ST = Cfg::kStages, TILES = D / 16;
+  constexpr int GW = 8 / R;                        // columns of a group
+  constexpr int SUB = R == 1 && CH > 1 ? 2 : 1;    // softmax passes between checks of the maximum
+  static_assert(CH % (R * SUB) == 0 && (R == 1 || NT == 1), "");
   constexpr float kL = (float)((1 << BITS) - 1);
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ __align__(8) uint64_t bars[kDecodeWarps][ST];
@@ -413,48 +423,62 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
   Piece ahead = piece;
   int aj = ahead.j0 + warp;
   bool more = true;
-  int pages[CH];
   const int per_page = a.c.page_size / kKvChunk;
+  const bool whole_blocks = per_page % CH == 0;  // a block's records lie side by side
+  int pages[CH];
+  auto page_of = [&](int c) { return a.page_shift >= 0 ? c >> a.page_shift : c / per_page; };
   auto settle = [&]() {  // move `ahead` to the warp's next block and read its pages' numbers
     while (more && aj >= ahead.j1) {
       more = ahead.next(a);
       aj = ahead.j0 + warp;
     }
     if (!more) return;
+    const int32_t* table = a.tables + (size_t)ahead.b * a.table_width;
+    pages[0] = table[page_of(aj * CH)];
+    if (!whole_blocks) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = aj * CH + i;
-      if (c * kKvChunk < ahead.len)
-        pages[i] = a.tables[(size_t)ahead.b * a.table_width + (a.page_shift >= 0 ? c >> a.page_shift : c / per_page)];
+      for (int i = 1; i < CH; ++i)
+        if ((aj * CH + i) * kKvChunk < ahead.len) pages[i] = table[page_of(aj * CH + i)];
     }
   };
   auto copy = [&](int stage) {
     if (!more) return;
     if (lane == 0) {
-      const int hk = ahead.h / a.groups;
-      const uint8_t* src[CH];
-      uint32_t bytes = 0;
+      const int hk = a.groups == 1 ? ahead.h : ahead.h / a.groups;
+      uint64_t* bar = &bars[warp][stage];
+      uint8_t* dst = ring + stage * Cfg::kStageBytes;
+      auto source = [&](int page, int c) {
+        const int in_page = a.page_shift >= 0 ? c & (per_page - 1) : c % per_page;
+        return a.c.base + (((size_t)page * a.c.Hkv + hk) * per_page + in_page) * (size_t)Rec::kBytes;
+      };
+      const int c0 = aj * CH, tokens = ahead.len - c0 * kKvChunk;  // > 0
+      if (whole_blocks) {
+        const bool good = pages[0] >= 0 && pages[0] < a.c.num_pages;
+        const int chunks = (tokens + kKvChunk - 1) / kKvChunk < CH ? (tokens + kKvChunk - 1) / kKvChunk : CH;
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = aj * CH + i;
-        int n = ahead.len - c * kKvChunk;
-        src[i] = nullptr;
-        if (n > 0) {
-          if (pages[i] >= 0 && pages[i] < a.c.num_pages) {
-            const int in_page = a.page_shift >= 0 ? c & (per_page - 1) : c % per_page;
-            src[i] = a.c.base + (((size_t)pages[i] * a.c.Hkv + hk) * per_page + in_page) * (size_t)Rec::kBytes;
-            bytes += Rec::kBytes;
-          } else {
-            raise_error(kErrBadIndex);
-            n = 0;
-          }
+        for (int i = 0; i < CH; ++i) {
+          const int n = tokens - i * kKvChunk;
+          valid[warp][stage][i] = !good || n < 0 ? 0 : n < kKvChunk ? n : kKvChunk;
         }
-        valid[warp][stage][i] = n < 0 ? 0 : n < kKvChunk ? n : kKvChunk;
-      }
-      mbar_arrive_expect_tx(&bars[warp][stage], bytes);
+        mbar_arrive_expect_tx(bar, good ? chunks * Rec::kBytes : 0);
+        if (good) bulk_load_1d(dst, source(pages[0], c0), chunks * Rec::kBytes, bar);
+        else raise_error(kErrBadIndex);
+      } else {
+        uint32_t bytes = 0;
+        bool good[CH];
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
-        if (src[i]) bulk_load_1d(ring + stage * Cfg::kStageBytes + i * Rec::kBytes, src[i], Rec::kBytes, &bars[warp][stage]);
+        for (int i = 0; i < CH; ++i) {
+          const int n = tokens - i * kKvChunk;
+          good[i] = n > 0 && pages[i] >= 0 && pages[i] < a.c.num_pages;
+          if (n > 0 && !good[i]) raise_error(kErrBadIndex);
+          valid[warp][stage][i] = !good[i] ? 0 : n < kKvChunk ? n : kKvChunk;
+          bytes += good[i] ? Rec::kBytes : 0;
+        }
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (good[i]) bulk_load_1d(dst + i * Rec::kBytes, source(pages[i], c0 + i), Rec::kBytes, bar);
+      }
     }
     aj += kDecodeWarps;
     settle();
@@ -482,8 +506,9 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
       uint32_t raw[QN / 2];
 #pragma unroll
       for (int i = 0; i < QN / 2; ++i) raw[i] = 0;
-      if (8 * n + g < nheads) {
-        const uint16_t* qp = a.Q + (size_t)piece.b * a.q_stride + (size_t)(head0 + 8 * n + g) * D +
+      const int qh = R == 1 ? 8 * n + g : g % GW;  // the column's head
+      if (qh < nheads) {
+        const uint16_t* qp = a.Q + (size_t)piece.b * a.q_stride + (size_t)(head0 + qh) * D +
                              (KP::kShared ? (j >> 1) * 32 : j * (D / 4));
         load_words<QN / 2>(reinterpret_cast<const uint8_t*>(qp), raw);
       }
@@ -534,7 +559,8 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
     }
 
     float acc[NT][TILES][4];
-    float m[NT][2], l[NT][2], wsum[NT][2];
+    float wsum[NT][4];  // sums of the rounded weights: a product with ones, every row of it the same
+    float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -542,106 +568,131 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, l[n][i] = 0.f, wsum[n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) wsum[n][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, l[n][i] = 0.f;
     }
 
     for (int bj = piece.j0 + warp; bj < piece.j1; bj += kDecodeWarps) {
       if (!mbar_wait(&bars[warp][pos.s], pos.ph, &abort_flag)) more = false;  // flagged: copy nothing more
       const uint8_t* stage = ring + pos.s * Cfg::kStageBytes;
-      float z[CH][NT][4];  // score + binade of gammaV
-      float down[CH][2], ratio[CH][2];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint8_t* rec = stage + c * Rec::kBytes;
-        const int nv = valid[warp][pos.s][c];
-        float s[NT][4];
+      for (int c0 = 0; c0 < CH; c0 += R * SUB) {
+        float z[SUB][NT][4];  // score + binade of gammaV
+        float down[SUB][2], ratio[SUB][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < SUB; ++u) {
+          float s[NT][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-        {
-          uint32_t k0[KP::kN], k1[KP::kN];
-          k_pairs<D, BITS>(rec + row0 * Rec::kRow, j, k0);
-          k_pairs<D, BITS>(rec + (row0 + 2) * Rec::kRow, j, k1);
-#pragma unroll
-          for (int t = 0; t < TILES; ++t)
+          for (int r = 0; r < R; ++r) {
+            const uint8_t* rec = stage + (c0 + u * R + r) * Rec::kBytes;
+            float sc[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              mma_f16_16816(s[n], k0[2 * t], k1[2 * t], k0[2 * t + 1], k1[2 * t + 1], qf[n][2 * t], qf[n][2 * t + 1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+            uint32_t k0[KP::kN], k1[KP::kN];
+            k_pairs<D, BITS>(rec + row0 * Rec::kRow, j, k0);
+            k_pairs<D, BITS>(rec + (row0 + 2) * Rec::kRow, j, k1);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16_16816(sc[n], k0[2 * t], k1[2 * t], k0[2 * t + 1], k1[2 * t + 1], qf[n][2 * t], qf[n][2 * t + 1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[n][i] = r == 0 || 2 * j / GW == r ? sc[n][i] : s[n][i];
+          }
+          const int mine = c0 + u * R + 2 * j / GW;  // the chunk of this lane's columns
+          const uint8_t* rec = stage + mine * Rec::kBytes;
+          const int nv = valid[warp][pos.s][mine];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = row0 + 2 * r;
+            const bool in = row < nv;
+            const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[row];
+            const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[row];
+            int e = (int)((__float_as_uint(gv) >> 23) & 0xffu);  // biased
+            e = e < 37 ? 37 : e > 253 ? 253 : e;
+            down[u][r] = __uint_as_float((uint32_t)(254 - e) << 23);
+            ratio[u][r] = in ? gv * down[u][r] : 0.f;
+            const float ef = __uint_as_float(0x4b000000u + (uint32_t)e) - (8388608.f + 127.f);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                z[u][n][2 * r + i] = in ? fmaf(gk, fmaf(cA[n][i], s[n][2 * r + i], -cB[n][i]), ef) : -INFINITY;
+          }
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = row0 + 2 * r;
-          const bool in = row < nv;
-          const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[row];
-          const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[row];
-          int e = (int)((__float_as_uint(gv) >> 23) & 0xffu) - 127;
-          e = e < -90 ? -90 : e > 126 ? 126 : e;
-          down[c][r] = __uint_as_float((uint32_t)(127 - e) << 23);
-          ratio[c][r] = in ? gv * down[c][r] : 0.f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              z[c][n][2 * r + i] = in ? fmaf(gk, fmaf(cA[n][i], s[n][2 * r + i], -cB[n][i]), (float)e) : -INFINITY;
-        }
-      }
-      // the running maximum moves only when a weight would pass 2^8 (fp16 holds up to 2^16)
-      bool grow = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < CH; ++c) grow |= fmaxf(z[c][n][i], z[c][n][2 + i]) > m[n][i] + 8.f;
-      if (__any_sync(0xffffffffu, grow)) {
+        // the running maximum moves only when a weight would pass 2^8 (fp16 holds up to 2^16)
+        bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = m[n][i];
-#pragma unroll
-            for (int c = 0; c < CH; ++c) top = fmaxf(top, fmaxf(z[c][n][i], z[c][n][2 + i]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float f = top == -INFINITY ? 1.f : ex2_approx(m[n][i] - top);
-            m[n][i] = top;
-            l[n][i] *= f;
-            wsum[n][i] *= f;
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              acc[n][t][i] *= f;
-              acc[n][t][2 + i] *= f;
-            }
+            float top = fmaxf(z[0][n][i], z[0][n][2 + i]);
+            if constexpr (SUB == 2) top = fmaxf(top, fmaxf(z[1][n][i], z[1][n][2 + i]));
+            grow |= top > m[n][i] + 8.f;
           }
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        uint32_t wb[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p = ex2_approx(z[c][n][2 * r + i] - (m[n][i] == -INFINITY ? 0.f : m[n][i]));
-              l[n][i] = fmaf(p, down[c][r], l[n][i]);
-              w[i] = p * ratio[c][r];
-            }
-            const __half2 h2 = __floats2half2_rn(w[0], w[1]);
-            const float2 f = __half22float2(h2);
-            wsum[n][0] += f.x;
-            wsum[n][1] += f.y;
-            wb[n][r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h2));
-          }
-        uint32_t va[VC::kN], vb[VC::kN];
-        v_codes<D, BITS>(stage + c * Rec::kBytes + Rec::kV, g, j, va, vb);
-#pragma unroll
-        for (int t = 0; t < TILES; ++t)
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma_f16_16816(acc[n][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], wb[n][0], wb[n][1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float top = m[n][i];
+#pragma unroll
+              for (int u = 0; u < SUB; ++u) top = fmaxf(top, fmaxf(z[u][n][i], z[u][n][2 + i]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const float f = top == -INFINITY ? 1.f : ex2_approx(m[n][i] - top);
+              m[n][i] = top;
+              l[n][i] *= f;
+              wsum[n][i] *= f;
+              wsum[n][2 + i] *= f;
+#pragma unroll
+              for (int t = 0; t < TILES; ++t) {
+                acc[n][t][i] *= f;
+                acc[n][t][2 + i] *= f;
+              }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          uint32_t wb[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float p = ex2_approx(z[u][n][2 * r + i] - (m[n][i] == -INFINITY ? 0.f : m[n][i]));
+                l[n][i] = fmaf(p, down[u][r], l[n][i]);
+                w[i] = p * ratio[u][r];
+              }
+              const __half2 h2 = __floats2half2_rn(w[0], w[1]);
+              wb[n][r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h2));
+            }
+            constexpr uint32_t kOnes = 0x3c003c00u;
+            mma_f16_16816(wsum[n], kOnes, kOnes, kOnes, kOnes, wb[n][0], wb[n][1]);
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            uint32_t va[VC::kN], vb[VC::kN];
+            v_codes<D, BITS>(stage + (c0 + u * R + r) * Rec::kBytes + Rec::kV, g, j, va, vb);
+            uint32_t wr[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) wr[n][i] = R == 1 || g / GW == r ? wb[n][i] : 0u;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16_16816(acc[n][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], wr[n][0], wr[n][1]);
+          }
+        }
       }
       __syncwarp();  // every lane is done with the stage
       copy(pos.s);
@@ -656,7 +707,6 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
-          wsum[n][i] += __shfl_xor_sync(0xffffffffu, wsum[n][i], o);
         }
         const int col = 8 * n + 2 * j + i;
         float* row = scratch + (warp * Cfg::kHeads + col) * Cfg::kRow;
@@ -676,20 +726,25 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
     __syncthreads();
     const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
     const bool whole = piece.j0 == 0 && piece.j1 == nb;
-    float* slot = a.ws + (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * a.group * (D + 2);
+    float* slot = a.ws + (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * a.group * (D + 4);
     for (int x = threadIdx.x; x < nheads * D; x += 32 * kDecodeWarps) {
-      const int col = x / D, y = x % D;
-      float top = merge_m[0][col];
+      const int col = x / D, y = x % D;  // the head's columns: col, col + GW, ...
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 1; w < kDecodeWarps; ++w) top = fmaxf(top, merge_m[w][col]);
+      for (int w = 0; w < kDecodeWarps; ++w)
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = fmaxf(top, merge_m[w][col + r * GW]);
       float o = 0.f, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w) {
-        if (merge_m[w][col] == -INFINITY) continue;  // a warp without a token in this piece
-        const float f = ex2_approx(merge_m[w][col] - top);
-        o = fmaf(f, scratch[(w * Cfg::kHeads + col) * Cfg::kRow + y], o);
-        sum = fmaf(f, merge_l[w][col], sum);
-      }
+      for (int w = 0; w < kDecodeWarps; ++w)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float mw = merge_m[w][col + r * GW];
+          if (mw == -INFINITY) continue;  // no token in this piece
+          const float f = ex2_approx(mw - top);
+          o = fmaf(f, scratch[(w * Cfg::kHeads + col + r * GW) * Cfg::kRow + y], o);
+          sum = fmaf(f, merge_l[w][col + r * GW], sum);
+        }
       const int d = VC::feature(y & 7, y >> 3);
       if (whole) {
         const size_t bh = (size_t)piece.b * a.Hq + head0 + col;
@@ -724,9 +779,16 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
   }
 }
 
-// The pieces of the chain that begins in the main kernel's CTA blockIdx.x, added in order. A CTA for
-// each head of the column block, a thread per feature.
-static __global__ void attn_decode_join_kernel(const DecodeAttnArgs a, int D) {
+constexpr int kJoinThreads = 256;
+
+// The pieces of the chain that begins in the main kernel's CTA blockIdx.x, added in a fixed order. A CTA
+// for each head of the column block; D / 4 threads take four features each, the groups of threads every
+// so many-th piece, so that a long chain's reads are in flight together.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const DecodeAttnArgs a) {
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+  __shared__ float f[kDecodeMaxCtas];
+  __shared__ float red[kJoinThreads / 32], parts[GROUPS][D];
   pdl_wait();
   pdl_launch_dependents();
   const DecodeChain ch = a.chains[blockIdx.x];
@@ -735,23 +797,54 @@ static __global__ void attn_decode_join_kernel(const DecodeAttnArgs a, int D) {
   const int b = ch.col / hcols, h = ch.col % hcols;
   const int col = blockIdx.y, in_kv = h % a.groups * a.group + col;
   if (in_kv >= G) return;
-  const size_t slot = (size_t)a.group * (D + 2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t slot = (size_t)a.group * (D + 4);
   const float* w0 = a.ws + 2 * blockIdx.x * slot;
   auto place = [&](int i) { return w0 + (2 * i + (i == 0 ? ch.first : 0)) * slot; };
   float top = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < ch.n; ++i) top = fmaxf(top, place(i)[a.group * D + col]);
-  float o = 0.f, sum = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < ch.n; ++i) {
-    const float* p = place(i);
-    const float mi = p[a.group * D + col];
-    const float f = mi == -INFINITY ? 0.f : ex2_approx(mi - top);
-    o = fmaf(f, p[col * D + threadIdx.x], o);
-    sum = fmaf(f, p[a.group * D + a.group + col], sum);
+  for (int i = threadIdx.x; i < ch.n; i += kJoinThreads) {
+    f[i] = place(i)[a.group * D + col];
+    top = fmaxf(top, f[i]);
   }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[w]);
+  __syncthreads();
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < ch.n; i += kJoinThreads) {
+    f[i] = f[i] == -INFINITY ? 0.f : ex2_approx(f[i] - top);
+    sum = fmaf(f[i], place(i)[a.group * D + a.group + col], sum);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) sum += red[w];
+  const int d0 = threadIdx.x % LANES * 4, group = threadIdx.x / LANES;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = group; i < ch.n; i += GROUPS) {
+    const float4 v = *reinterpret_cast<const float4*>(place(i) + col * D + d0);
+    o[0] = fmaf(f[i], v.x, o[0]);
+    o[1] = fmaf(f[i], v.y, o[1]);
+    o[2] = fmaf(f[i], v.z, o[2]);
+    o[3] = fmaf(f[i], v.w, o[3]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) parts[group][d0 + e] = o[e];
+  __syncthreads();
   const size_t bh = (size_t)b * a.Hq + h / a.groups * G + in_kv;
-  a.O[bh * D + threadIdx.x] = (uint16_t)(pack_bf16(sum > 0.f ? o / sum : 0.f, 0.f) & 0xffffu);
+  if (threadIdx.x < D) {
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) y += parts[i][threadIdx.x];
+    a.O[bh * D + threadIdx.x] = (uint16_t)(pack_bf16(sum > 0.f ? y / sum : 0.f, 0.f) & 0xffffu);
+  }
   if (threadIdx.x == 0 && a.lse) a.lse[bh] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 

@@ -73,11 +73,11 @@ int decode_group(int G, int D) {
   return (G + passes - 1) / passes;
 }
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT, int R>
 hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   using Cfg = DecodeCfg<D, BITS, NT>;
   static SmemLimit lim;
-  auto* k = attn_decode_kernel<D, BITS, NT>;
+  auto* k = attn_decode_kernel<D, BITS, NT, R>;
   const cudaError_t e = allow_smem(k, Cfg::kSmem, lim);
   if (e != cudaSuccess) return cuda_fail(e);
   // every CTA resident at once, and no more than the tables have room for
@@ -89,7 +89,7 @@ hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   if (want < grid) grid = (int)want;
   const hbl_status st = launch_pdl(k, dim3(grid), dim3(32 * kDecodeWarps), Cfg::kSmem, s, a);
   if (st != HBL_OK) return st;
-  return launch_pdl(attn_decode_join_kernel, dim3(grid, a.group), dim3(D), 0, s, a, D);
+  return launch_pdl(attn_decode_join_kernel<D>, dim3(grid, a.group), dim3(kJoinThreads), 0, s, a);
 }
 
 // bf16 states [T][H][D] with rows `stride` elements apart, in boxes of 64 features, `heads` heads and
@@ -211,7 +211,7 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
 
 size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
-  return round_up(kDecodeMaxCtas * (sizeof(DecodeChain) + (size_t)2 * decode_group(Hq / Hkv, D) * (D + 2) * sizeof(float)), 256);
+  return round_up(kDecodeMaxCtas * (sizeof(DecodeChain) + (size_t)2 * decode_group(Hq / Hkv, D) * (D + 4) * sizeof(float)), 256);
 }
 
 hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, size_t cache_bytes, int num_pages,
@@ -247,10 +247,18 @@ hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, si
   a.ws = reinterpret_cast<float*>(a.chains + kDecodeMaxCtas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return for_head(D, bits, [&](auto d, auto b) {
+    // groups of columns for as many chunks as the heads leave room for, and a block has
+    constexpr int chunks = DecodeCfg<d(), b(), 1>::kChunks;
     if constexpr (d() <= 128) {
-      if (a.group > 8) return launch_decode_attn<d(), b(), 2>(a, s);
+      if (a.group > 8) return launch_decode_attn<d(), b(), 2, 1>(a, s);
     }
-    return launch_decode_attn<d(), b(), 1>(a, s);
+    if constexpr (chunks >= 4) {
+      if (a.group <= 2) return launch_decode_attn<d(), b(), 1, 4>(a, s);
+    }
+    if constexpr (chunks >= 2) {
+      if (a.group <= 4) return launch_decode_attn<d(), b(), 1, 2>(a, s);
+    }
+    return launch_decode_attn<d(), b(), 1, 1>(a, s);
   });
 }
 
