@@ -31,9 +31,10 @@
 // zeroed for the product with a chunk's V, and the groups are joined like the pieces of the warps.
 //
 // Split: the (sequence, KV head, 64-token block) triples of the whole batch are laid end to end and
-// divided evenly over the CTAs, whatever the lengths; a piece of a sequence that a CTA does not hold
-// alone leaves (max, sum, o) in the workspace and attn_decode_join_kernel adds the pieces in order.
-// Inside a CTA each warp takes every fourth block of a piece through its own ring of bulk copies.
+// divided evenly over the warps, whatever the lengths. A warp passes its blocks through a ring of its own
+// and never waits for another one: a piece of a sequence that it does not hold alone goes to the workspace
+// as (max, sum, o), and attn_decode_join_kernel adds the pieces in order. (Joining the four warps of a CTA
+// at each piece's end instead cost a ragged batch of 64 sequences 84 us against @RAGGED@.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -45,13 +46,12 @@ namespace hbl {
 
 constexpr int kDecodeMaxB = 4096;   // sequences of one call
 constexpr int kDecodeWarps = 4;
-constexpr int kDecodeMaxCtas = 640;  // bounds the workspace
+constexpr int kDecodeMaxUnits = 4 * 448;  // warps that share the work; bounds the workspace
 
-// The pieces of a (sequence, column block) that begins in a CTA and ends in a later one.
+// Where the pieces of a (sequence, column block) are.
 struct DecodeChain {
-  int col;    // sequence * column blocks + column block; -1: none begins here
-  int n;      // CTAs
-  int first;  // 0: it is the CTA's first piece, 1: its last
+  int unit, n;  // first warp's number, number of warps (1: the output is written already)
+  int first;    // 0: it is that warp's first piece, 1: its last
   int pad;
 };
 
@@ -66,25 +66,21 @@ struct DecodeAttnArgs {
   int B, Hq;
   int group, groups;  // query heads per block of columns; blocks per KV head
   float scale;        // scale * log2(e) / L
-  int min_blocks;     // per CTA
   uint16_t* O;        // bf16 [B][Hq][D]
   float* lse;         // [B][Hq] or nullptr
-  DecodeChain* chains;  // [CTAs]
-  float* ws;            // [CTAs][2][group][D + 4]: a CTA's first piece, then its last
+  DecodeChain* chains;  // [B][Hkv * groups]
+  float* ws;            // [units][2][group][D + 4]: a warp's first piece, then its last
 };
 
 template <int D, int BITS, int NT>
 struct DecodeCfg {
   using Rec = KvRec<D, BITS>;
-  // records per block of the ring: the warps' two stages within about 70 KB
+  // records per block of the ring: the warps' two stages each within about 70 KB
   static constexpr int kChunks = Rec::kBytes <= 2304 ? 4 : Rec::kBytes <= 4608 ? 2 : 1;
   static constexpr int kBlock = 16 * kChunks;  // tokens
   static constexpr int kStageBytes = kChunks * Rec::kBytes;
   static constexpr int kStages = 2;
-  static constexpr int kHeads = 8 * NT;
-  static constexpr int kRow = D + 4;  // floats of a head's row in the merge scratch
-  static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRing + kDecodeWarps * kHeads * kRow * 4;
+  static constexpr int kSmem = kDecodeWarps * kStages * kStageBytes;
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -130,7 +126,7 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t* out) {
 
 // Three bits: the pair of codes in the bits 15 of three words.
 __device__ __forceinline__ uint32_t spare_pair(uint32_t w0, uint32_t w1, uint32_t w2) {
-  return ((w0 >> 15) & 0x00010001u) | ((w1 >> 14) & 0x00020002u) | ((w2 >> 13) & 0x00040004u);
+  return (((w0 >> 2) & 0x20002000u) | ((w1 >> 1) & 0x40004000u) | (w2 & 0x80008000u)) >> 13;
 }
 
 // Lane j (0..3) of a quad holds a quarter of a K row's features as D/8 pairs; pair i holds features
@@ -281,15 +277,10 @@ __device__ __forceinline__ int decode_len(const DecodeAttnArgs& a, int b) {
   return n < 0 ? 0 : n > most ? (int)most : n;
 }
 
-// First block of CTA i of n, of `total` blocks.
+// First block of warp i of n, of `total` blocks.
 __device__ __forceinline__ long long decode_first(long long total, int i, int n) { return total * i / n; }
 
-__device__ __forceinline__ int decode_ctas(long long total, int min_blocks, int grid) {
-  const long long want = (total + min_blocks - 1) / min_blocks;
-  return want < grid ? (int)want : grid;
-}
-
-// A piece: blocks j0 .. j1-1 of (sequence b, column block h); `rest` blocks of the CTA follow it.
+// A piece: blocks j0 .. j1-1 of (sequence b, column block h); `rest` blocks of the warp follow it.
 template <int BLOCK>
 struct DecodePiece {
   int b, h, j0, j1, len;
@@ -300,7 +291,7 @@ struct DecodePiece {
     j1 = rest < n ? j0 + (int)rest : nb;
     rest -= j1 - j0;
   }
-  // the next piece; false at the end of the CTA's blocks
+  // the next piece; false at the end of the warp's blocks
   __device__ __forceinline__ bool next(const DecodeAttnArgs& a) {
     if (rest <= 0) return false;
     if (++h == a.c.Hkv * a.groups) {
@@ -319,7 +310,7 @@ struct DecodePiece {
 
 // R groups of 8 / R columns, each for another chunk (R = 1 where NT = 2).
 template <int D, int BITS, int NT, int R>
-__global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const DecodeAttnArgs a) {
+__global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2) attn_decode_kernel(const DecodeAttnArgs a) {
   using Cfg = DecodeCfg<D, BITS, NT>;
   using Rec = KvRec<D, BITS>;
   using KP = KPairs<D, BITS>;
@@ -333,12 +324,10 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ __align__(8) uint64_t bars[kDecodeWarps][ST];
   __shared__ int valid[kDecodeWarps][ST][CH];  // tokens of each chunk that count
-  __shared__ float merge_m[kDecodeWarps][Cfg::kHeads], merge_l[kDecodeWarps][Cfg::kHeads];
   __shared__ long long scan[kDecodeWarps];
-  __shared__ int start_b;
-  __shared__ long long start_off;
+  __shared__ int start_b[kDecodeWarps];
+  __shared__ long long start_off[kDecodeWarps];
   __shared__ volatile int abort_flag;
-  float* scratch = reinterpret_cast<float*>(dec_smem + Cfg::kRing);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, j = lane & 3;
@@ -346,7 +335,6 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    start_b = -1;
     for (int w = 0; w < kDecodeWarps; ++w)
       for (int s = 0; s < ST; ++s) mbar_init(&bars[w][s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -354,7 +342,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
   pdl_wait();
   pdl_launch_dependents();
 
-  // the batch's blocks, and where this CTA's begin: a thread sums a run of consecutive sequences
+  // the batch's blocks, and where each warp's begin: a thread sums a run of consecutive sequences
   const int run = (a.B + 32 * kDecodeWarps - 1) / (32 * kDecodeWarps);
   const int b_lo = threadIdx.x * run, b_hi = b_lo + run < a.B ? b_lo + run : a.B;
   long long mine = 0;
@@ -378,59 +366,61 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
     total += scan[w];
   }
   total *= hcols;
-  const int ctas = decode_ctas(total, a.min_blocks, gridDim.x);
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {  // empty sequences
     if (decode_len(a, b) > 0) continue;
     for (int x = threadIdx.x; x < a.Hq * D / 2; x += 32 * kDecodeWarps)
       reinterpret_cast<uint32_t*>(a.O + (size_t)b * a.Hq * D)[x] = 0;
     if (a.lse)
       for (int x = threadIdx.x; x < a.Hq; x += 32 * kDecodeWarps) a.lse[(size_t)b * a.Hq + x] = -INFINITY;
+    for (int x = threadIdx.x; x < hcols; x += 32 * kDecodeWarps) a.chains[(size_t)b * hcols + x].n = 1;
   }
-  if ((int)blockIdx.x >= ctas) {
-    if (threadIdx.x == 0) a.chains[blockIdx.x].col = -1;
-    return;
-  }
-  const long long first = decode_first(total, blockIdx.x, ctas), last = decode_first(total, blockIdx.x + 1, ctas);
-  {
+  const int units = total < (long long)gridDim.x * kDecodeWarps ? (int)total : gridDim.x * kDecodeWarps;
+  // consecutive units in different CTAs: few units keep all SMs busy
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    const int unit = w * gridDim.x + blockIdx.x;
+    if (unit >= units) break;
+    const long long first = decode_first(total, unit, units);
     long long at = (upto - mine) * hcols;
-    if (first >= at && first < upto * hcols) {
-      for (int b = b_lo; b < b_hi; ++b) {
-        const long long n = (long long)((decode_len(a, b) + Cfg::kBlock - 1) / Cfg::kBlock) * hcols;
-        if (first < at + n) {
-          start_b = b;
-          start_off = first - at;
-          break;
-        }
-        at += n;
+    if (first < at || first >= upto * hcols) continue;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = (long long)((decode_len(a, b) + Cfg::kBlock - 1) / Cfg::kBlock) * hcols;
+      if (first < at + n) {
+        start_b[w] = b;
+        start_off[w] = first - at;
+        break;
       }
+      at += n;
     }
   }
   __syncthreads();
-  if (start_b < 0) return;  // unreachable: first < total
+  const int unit = warp * gridDim.x + blockIdx.x;
+  if (unit >= units) return;
+  const long long last = decode_first(total, unit + 1, units);
   Piece piece;
-  piece.b = start_b;
+  piece.b = start_b[warp];
   piece.len = decode_len(a, piece.b);
   {
     const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
-    piece.h = (int)(start_off / nb);
-    piece.j0 = (int)(start_off % nb);
-    piece.rest = last - first;
+    piece.h = (int)(start_off[warp] / nb);
+    piece.j0 = (int)(start_off[warp] % nb);
+    piece.rest = last - decode_first(total, unit, units);
     piece.cut();
   }
 
   // ---- this warp's ring of blocks, copied ahead of the products
   uint8_t* ring = dec_smem + warp * ST * Cfg::kStageBytes;
   Piece ahead = piece;
-  int aj = ahead.j0 + warp;
+  int aj = ahead.j0;  // the next block of `ahead`
   bool more = true;
   const int per_page = a.c.page_size / kKvChunk;
   const bool whole_blocks = per_page % CH == 0;  // a block's records lie side by side
   int pages[CH];
   auto page_of = [&](int c) { return a.page_shift >= 0 ? c >> a.page_shift : c / per_page; };
   auto settle = [&]() {  // move `ahead` to the warp's next block and read its pages' numbers
-    while (more && aj >= ahead.j1) {
-      more = ahead.next(a);
-      aj = ahead.j0 + warp;
+    if (aj == ahead.j1) {
+      more = more && ahead.next(a);
+      aj = 0;
     }
     if (!more) return;
     const int32_t* table = a.tables + (size_t)ahead.b * a.table_width;
@@ -480,7 +470,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
           if (good[i]) bulk_load_1d(dst + i * Rec::kBytes, source(pages[i], c0 + i), Rec::kBytes, bar);
       }
     }
-    aj += kDecodeWarps;
+    ++aj;
     settle();
   };
   settle();
@@ -573,7 +563,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
       for (int i = 0; i < 2; ++i) m[n][i] = -INFINITY, l[n][i] = 0.f;
     }
 
-    for (int bj = piece.j0 + warp; bj < piece.j1; bj += kDecodeWarps) {
+    for (int at = piece.j0; at < piece.j1; ++at) {
       if (!mbar_wait(&bars[warp][pos.s], pos.ph, &abort_flag)) more = false;  // flagged: copy nothing more
       const uint8_t* stage = ring + pos.s * Cfg::kStageBytes;
 #pragma unroll
@@ -657,6 +647,11 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
               }
             }
         }
+        float base[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) base[n][i] = m[n][i] == -INFINITY ? 0.f : m[n][i];
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
           uint32_t wb[NT][2];
@@ -667,7 +662,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
               float w[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float p = ex2_approx(z[u][n][2 * r + i] - (m[n][i] == -INFINITY ? 0.f : m[n][i]));
+                const float p = ex2_approx(z[u][n][2 * r + i] - base[n][i]);
                 l[n][i] = fmaf(p, down[u][r], l[n][i]);
                 w[i] = p * ratio[u][r];
               }
@@ -699,107 +694,113 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) attn_decode_kernel(const De
       pos.advance(1, ST);
     }
 
-    // ---- join the warps: o, sum and maximum of each head
+    // ---- join the column groups, then the output or the piece's part of it
+    const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
+    const bool whole = piece.j0 == 0 && piece.j1 == nb;
+    float* slot = a.ws + (size_t)(2 * unit + (first_piece ? 0 : 1)) * a.group * (D + 4);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
+        for (int o = 4; o < 32; o <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], o);
+        if constexpr (R > 1) {  // the groups' columns of a head lie 8 / R apart: lanes j, j ^ 2 (, j ^ 1)
+          float top = m[n][i];
+#pragma unroll
+          for (int o = GW / 2; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float f = m[n][i] == -INFINITY ? 0.f : ex2_approx(m[n][i] - top);
+          m[n][i] = top;
+          auto sum = [&](float& x) {
+            x *= f;
+#pragma unroll
+            for (int o = GW / 2; o < 4; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          };
+          sum(l[n][i]);
+          sum(wsum[n][i]);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            sum(acc[n][t][i]);
+            sum(acc[n][t][2 + i]);
+          }
         }
         const int col = 8 * n + 2 * j + i;
-        float* row = scratch + (warp * Cfg::kHeads + col) * Cfg::kRow;
-#pragma unroll
-        for (int t = 0; t < TILES; ++t)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int c = 2 * t + r;
-            const float up = 33554432.f / (kL * (float)(1 << VC::place(c)));
-            row[c * 8 + g] = fmaf(acc[n][t][2 * r + i], up, -wsum[n][i]);
-          }
-        if (g == 0) {
-          merge_m[warp][col] = m[n][i];
-          merge_l[warp][col] = l[n][i];
-        }
-      }
-    __syncthreads();
-    const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
-    const bool whole = piece.j0 == 0 && piece.j1 == nb;
-    float* slot = a.ws + (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * a.group * (D + 4);
-    for (int x = threadIdx.x; x < nheads * D; x += 32 * kDecodeWarps) {
-      const int col = x / D, y = x % D;  // the head's columns: col, col + GW, ...
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w)
-#pragma unroll
-        for (int r = 0; r < R; ++r) top = fmaxf(top, merge_m[w][col + r * GW]);
-      float o = 0.f, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float mw = merge_m[w][col + r * GW];
-          if (mw == -INFINITY) continue;  // no token in this piece
-          const float f = ex2_approx(mw - top);
-          o = fmaf(f, scratch[(w * Cfg::kHeads + col + r * GW) * Cfg::kRow + y], o);
-          sum = fmaf(f, merge_l[w][col + r * GW], sum);
-        }
-      const int d = VC::feature(y & 7, y >> 3);
-      if (whole) {
+        if (2 * j >= GW || col >= nheads) continue;
         const size_t bh = (size_t)piece.b * a.Hq + head0 + col;
-        a.O[bh * D + d] = (uint16_t)(pack_bf16(sum > 0.f ? o / sum : 0.f, 0.f) & 0xffffu);
-        if (y == 0 && a.lse) a.lse[bh] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
-      } else {
-        slot[col * D + d] = o;
-        if (y == 0) {
-          slot[a.group * D + col] = top;
-          slot[a.group * D + a.group + col] = sum;
+        const float inv = !whole ? 1.f : l[n][i] > 0.f ? 1.f / l[n][i] : 0.f;
+        auto value = [&](int c) {  // feature number c of this lane
+          const float up = 33554432.f / (kL * (float)(1 << VC::place(c)));
+          return fmaf(acc[n][c >> 1][2 * (c & 1) + i], up, -wsum[n][i]) * inv;
+        };
+        constexpr int RUN = VC::kShared ? 1 : BITS == 8 ? 2 : 4;  // consecutive features
+#pragma unroll
+        for (int c = 0; c < VC::kN; c += RUN) {
+          const int d = VC::feature(g, c);
+          if (whole) {
+            uint16_t* o = a.O + bh * D + d;
+            if constexpr (RUN == 4) {
+              *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(value(c), value(c + 1)), pack_bf16(value(c + 2), value(c + 3)));
+            } else if constexpr (RUN == 2) {
+              *reinterpret_cast<uint32_t*>(o) = pack_bf16(value(c), value(c + 1));
+            } else {
+              *o = (uint16_t)(pack_bf16(value(c), 0.f) & 0xffffu);
+            }
+          } else {
+            float* o = slot + col * D + d;
+            if constexpr (RUN == 4) {
+              *reinterpret_cast<float4*>(o) = make_float4(value(c), value(c + 1), value(c + 2), value(c + 3));
+            } else if constexpr (RUN == 2) {
+              *reinterpret_cast<float2*>(o) = make_float2(value(c), value(c + 1));
+            } else {
+              *o = value(c);
+            }
+          }
+        }
+        if (g == 0) {
+          if (!whole) {
+            slot[a.group * D + col] = m[n][i];
+            slot[a.group * D + a.group + col] = l[n][i];
+          } else if (a.lse) {
+            a.lse[bh] = l[n][i] > 0.f ? (m[n][i] + log2f(l[n][i])) * 0.69314718055994530942f : -INFINITY;
+          }
         }
       }
-    }
-    const DecodePiece<Cfg::kBlock> done = piece;
-    if (!piece.next(a)) {
-      if (threadIdx.x == 0) {
-        DecodeChain ch = {-1, 0, first_piece ? 0 : 1, 0};
-        if (done.j0 == 0 && done.j1 < nb) {
-          const long long end = last + nb - done.j1;  // of its blocks
-          int i1 = (int)((end - 1) * ctas / total);   // the last CTA whose first block is below it
-          while (i1 + 1 < ctas && decode_first(total, i1 + 1, ctas) < end) ++i1;
-          while (decode_first(total, i1, ctas) >= end) --i1;
-          ch.col = done.b * hcols + done.h;
-          ch.n = i1 - (int)blockIdx.x + 1;
-        }
-        a.chains[blockIdx.x] = ch;
+    if (piece.j0 == 0 && lane == 0) {  // the pieces of the sequence that begins here
+      DecodeChain ch = {unit, 1, first_piece ? 0 : 1, 0};
+      if (!whole) {
+        const long long end = last + nb - piece.j1;  // of its blocks: this piece is the warp's last
+        int i1 = (int)((end - 1) * units / total);   // the last warp whose first block is below it
+        while (i1 + 1 < units && decode_first(total, i1 + 1, units) < end) ++i1;
+        while (decode_first(total, i1, units) >= end) --i1;
+        ch.n = i1 - unit + 1;
       }
-      break;
+      a.chains[(size_t)piece.b * hcols + piece.h] = ch;
     }
+    if (!piece.next(a)) break;
     first_piece = false;
-    __syncthreads();  // before the scratch is written again
   }
 }
 
 constexpr int kJoinThreads = 256;
 
-// The pieces of the chain that begins in the main kernel's CTA blockIdx.x, added in a fixed order. A CTA
-// for each head of the column block; D / 4 threads take four features each, the groups of threads every
-// so many-th piece, so that a long chain's reads are in flight together.
+// The pieces of (sequence, column block) blockIdx.x, added in a fixed order. A CTA for each head of the
+// column block; D / 4 threads take four features each, the groups of threads every so many-th piece, so
+// that a long chain's reads are in flight together.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const DecodeAttnArgs a) {
   constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
-  __shared__ float f[kDecodeMaxCtas];
+  __shared__ float f[kDecodeMaxUnits];
   __shared__ float red[kJoinThreads / 32], parts[GROUPS][D];
   pdl_wait();
   pdl_launch_dependents();
   const DecodeChain ch = a.chains[blockIdx.x];
-  if (ch.col < 0) return;
+  if (ch.n <= 1) return;
   const int G = a.Hq / a.c.Hkv, hcols = a.c.Hkv * a.groups;
-  const int b = ch.col / hcols, h = ch.col % hcols;
+  const int b = blockIdx.x / hcols, h = blockIdx.x % hcols;
   const int col = blockIdx.y, in_kv = h % a.groups * a.group + col;
   if (in_kv >= G) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t slot = (size_t)a.group * (D + 4);
-  const float* w0 = a.ws + 2 * blockIdx.x * slot;
+  const float* w0 = a.ws + 2 * (size_t)ch.unit * slot;
   auto place = [&](int i) { return w0 + (2 * i + (i == 0 ? ch.first : 0)) * slot; };
   float top = -INFINITY;
   for (int i = threadIdx.x; i < ch.n; i += kJoinThreads) {

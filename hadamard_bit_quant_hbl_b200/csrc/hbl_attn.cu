@@ -82,14 +82,13 @@ hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   if (e != cudaSuccess) return cuda_fail(e);
   // every CTA resident at once, and no more than the tables have room for
   const long long blocks = ((long long)a.table_width * a.c.page_size + Cfg::kBlock - 1) / Cfg::kBlock;
-  a.min_blocks = kDecodeWarps;
-  const long long want = (blocks * a.B * a.c.Hkv * a.groups + a.min_blocks - 1) / a.min_blocks;
+  const long long want = blocks * a.B * a.c.Hkv * a.groups;
   int grid = resident_ctas(k, 32 * kDecodeWarps, Cfg::kSmem, lim);
-  if (grid > kDecodeMaxCtas) grid = kDecodeMaxCtas;
+  if (grid > kDecodeMaxUnits / kDecodeWarps) grid = kDecodeMaxUnits / kDecodeWarps;
   if (want < grid) grid = (int)want;
   const hbl_status st = launch_pdl(k, dim3(grid), dim3(32 * kDecodeWarps), Cfg::kSmem, s, a);
   if (st != HBL_OK) return st;
-  return launch_pdl(attn_decode_join_kernel<D>, dim3(grid, a.group), dim3(kJoinThreads), 0, s, a);
+  return launch_pdl(attn_decode_join_kernel<D>, dim3((unsigned)(a.B * a.c.Hkv * a.groups), a.group), dim3(kJoinThreads), 0, s, a);
 }
 
 // bf16 states [T][H][D] with rows `stride` elements apart, in boxes of 64 features, `heads` heads and
@@ -211,7 +210,10 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
 
 size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
-  return round_up(kDecodeMaxCtas * (sizeof(DecodeChain) + (size_t)2 * decode_group(Hq / Hkv, D) * (D + 4) * sizeof(float)), 256);
+  const int G = Hq / Hkv, group = decode_group(G, D), groups = (G + group - 1) / group;
+  return round_up((size_t)B * Hkv * groups * sizeof(DecodeChain) +
+                      (size_t)kDecodeMaxUnits * 2 * group * (D + 4) * sizeof(float),
+                  256);
 }
 
 hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, size_t cache_bytes, int num_pages,
@@ -244,7 +246,7 @@ hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, si
   a.O = static_cast<uint16_t*>(O);
   a.lse = lse;
   a.chains = static_cast<DecodeChain*>(workspace);
-  a.ws = reinterpret_cast<float*>(a.chains + kDecodeMaxCtas);
+  a.ws = reinterpret_cast<float*>(a.chains + (size_t)B * Hkv * a.groups);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return for_head(D, bits, [&](auto d, auto b) {
     // groups of columns for as many chunks as the heads leave room for, and a block has
