@@ -88,7 +88,11 @@ hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   if (want < grid) grid = (int)want;
   const hbl_status st = launch_pdl(k, dim3(grid), dim3(32 * kDecodeWarps), Cfg::kSmem, s, a);
   if (st != HBL_OK) return st;
-  return launch_pdl(attn_decode_join_kernel<D>, dim3((unsigned)(a.B * a.c.Hkv * a.groups), a.group), dim3(kJoinThreads), 0, s, a);
+  // few heads have long chains: more threads read a chain's pieces at once
+  const dim3 joins((unsigned)(a.B * a.c.Hkv * a.groups), a.group);
+  return (long long)joins.x * joins.y <= 256
+             ? launch_pdl(attn_decode_join_kernel<D, 1024>, joins, dim3(1024), 0, s, a)
+             : launch_pdl(attn_decode_join_kernel<D, 256>, joins, dim3(256), 0, s, a);
 }
 
 // bf16 states [T][H][D] with rows `stride` elements apart, in boxes of 64 features, `heads` heads and
@@ -172,19 +176,25 @@ hbl_status hbl_kv_append(const void* Q, size_t q_stride, const void* K, size_t k
   const int tiles = (T + kAppendTokens - 1) / kAppendTokens;
   const int heads = Hq + 2 * Hkv;
   // a CTA takes more heads (and builds the table of angles for more of them) as far as the tiles
-  // alone fill the device
+  // alone fill the device several times over
   int dev = 0;
   cudaGetDevice(&dev);
-  const int want = 4 * device_sms(dev);
-  int groups = want / tiles < 1 ? 1 : want / tiles;
-  if (groups > (heads + 3) / 4) groups = (heads + 3) / 4;
-  a.heads_per_cta = (heads + groups - 1) / groups;
-  groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
+  const int per_pass = kv_append_threads(D, bits) / 32 * (256 / D);  // heads that a CTA's warps take at once
+  const int passes = (heads + per_pass - 1) / per_pass;
+  const int want = 12 * device_sms(dev) / tiles;
+  if (want <= passes) {
+    a.heads_per_cta = (passes + want - 1) / (want < 1 ? 1 : want) * per_pass;
+    if (want < 1) a.heads_per_cta = passes * per_pass;
+  } else {  // few tokens: fewer heads than the warps could take, for the time of one pass
+    a.heads_per_cta = (heads + want - 1) / want;
+    if (a.heads_per_cta < 256 / D) a.heads_per_cta = 256 / D;
+  }
+  const int groups = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
   const dim3 grid(tiles, groups);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return for_head(D, bits, [&](auto d, auto b) {
-    return pos ? launch_pdl(kv_append_kernel<d(), b(), true>, grid, dim3(kAppendThreads), 0, s, a)
-               : launch_pdl(kv_append_kernel<d(), b(), false>, grid, dim3(kAppendThreads), 0, s, a);
+    return pos ? launch_pdl(kv_append_kernel<d(), b(), true>, grid, dim3(kv_append_threads(d(), b())), 0, s, a)
+               : launch_pdl(kv_append_kernel<d(), b(), false>, grid, dim3(kv_append_threads(d(), b())), 0, s, a);
   });
 }
 
@@ -203,8 +213,14 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
   a.V = static_cast<uint16_t*>(V);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return for_head(D, bits, [&](auto d, auto b) {
-    return launch_pdl(kv_gather_kernel<d(), b()>, dim3((T + kGatherTokens - 1) / kGatherTokens, Hkv),
-                      dim3(2 * kGatherTokens * d() / 16), 0, s, a);
+    // a CTA takes more heads (and finds its tokens' records for them) as far as the tokens alone fill
+    // the device
+    const int tiles = (T + kGatherTokens - 1) / kGatherTokens, pairs = (Hkv + kGatherHeads - 1) / kGatherHeads;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int want = 16 * device_sms(dev) / tiles;
+    return launch_pdl(kv_gather_kernel<d(), b()>, dim3(tiles, want < 1 ? 1 : want < pairs ? want : pairs),
+                      dim3(kGatherHeads * 2 * kGatherTokens * d() / 32), 0, s, a);
   });
 }
 
