@@ -181,7 +181,7 @@ hbl_status hbl_kv_append(const void* Q, size_t q_stride, const void* K, size_t k
   cudaGetDevice(&dev);
   const int per_pass = kv_append_threads(D, bits) / 32 * (256 / D);  // heads that a CTA's warps take at once
   const int passes = (heads + per_pass - 1) / per_pass;
-  const int want = 12 * device_sms(dev) / tiles;
+  const int want = 8 * device_sms(dev) / tiles;
   if (want <= passes) {
     a.heads_per_cta = (passes + want - 1) / (want < 1 ? 1 : want) * per_pass;
     if (want < 1) a.heads_per_cta = passes * per_pass;

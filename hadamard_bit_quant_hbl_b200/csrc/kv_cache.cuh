@@ -180,7 +180,7 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
 // that the codes are those of a 64-bit evaluation. A lane's eight values go two at a time through the
 // multiply-adds.
 template <int D, int BITS, bool ROPE>
-__global__ void __launch_bounds__(kv_append_threads(D, BITS), 3) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kernel(const KvAppendArgs a) {
   using Rec = KvRec<D, BITS>;
   using Pack = KvPack<BITS>;
   constexpr int HALF = D / 2;
@@ -319,12 +319,25 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 3) kv_append_kerne
         bool near = kind != 0 && !(range && far <= 0.5f - kNear);
         if (near) {
           // A zero is L/2 exactly, which the fp32 rounding takes to the even code: no border case,
-          // unless it comes from a rotation that cancelled.
+          // unless it comes from a rotation that cancelled. A state that was not rotated lies on the border
+          // above code k where L x = (2k + 1 - L) gamma, and bf16 values often do (for three bits whenever
+          // gamma's significand divides by 7): both sides are exact in fp32. Left for 64 bits is the
+          // border of code L/2 with a state so small that 64 bits may round it away.
+          const bool turned = ROPE && kind < 2;
           near = !range;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const bool zero = v[e] == 0.f && (!ROPE || kind == 2 || v[e ^ 4] == 0.f);
-            near |= !zero && fabsf(d[e]) > 0.5f - kNear;
+            const bool zero = v[e] == 0.f && (!turned || v[e ^ 4] == 0.f);
+            if (zero || fabsf(d[e]) <= 0.5f - kNear) continue;
+            const float tt = fmaf(w[e], mult, 0.5f * kL);
+            const float k = rintf(tt - 0.5f), border = 2.f * k + 1.f - kL;
+            if (turned || border == 0.f) {
+              near = true;
+            } else {
+              const float at = kL * v[e] - border * g;
+              const float odd = k - 2.f * floorf(0.5f * k);
+              y[e] = __float_as_uint(k + (at > 0.f || (at == 0.f && odd != 0.f) ? 1.f : 0.f) + kMagic);
+            }
           }
         }
         if (__any_sync(0xffffffffu, near)) {
