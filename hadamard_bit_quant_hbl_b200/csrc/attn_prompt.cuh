@@ -20,10 +20,12 @@
 // row, so its statistics need no exchange.
 //
 //   warps 0-3 (4-7)  softmax of the first (second) tile, then its output
-//   next warp        issues the products: while one tile is in its softmax, the other's P V and the next
-//                    S run. Rows of V behind a sequence's last key, which may hold anything, are
-//                    cleared in shared memory (the scores of such keys are replaced by -inf)
-//   last warp        TMA copies of Q, then of K and V blocks through a ring
+//   a warp per tile  one thread issues the tile's products: while one tile is in its softmax, the other's
+//                    P V and next S run. (One thread for both tiles was the limit: issuing a tile's 16
+//                    products took it 1300 to 1600 clocks next to the softmax warps, and each wait 200.)
+//   last warp        TMA copies of Q, then of K and V blocks through a ring. Rows of V behind a sequence's
+//                    last key, which may hold anything, are cleared in shared memory (the scores of such
+//                    keys are replaced by -inf)
 //
 // One CTA per SM; a launch has a CTA per (tile pair, head group), the pairs of most keys first. Sizes of
 // sequences are read on the device: a CTA finds its tile from the borders.
@@ -68,16 +70,16 @@ __device__ __forceinline__ bool prompt_borders(const PromptAttnArgs& a, int b, i
 template <int D>
 struct PromptCfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;
-  static constexpr int kKeys = D == 256 ? 64 : 128;  // of a block
+  static constexpr int kKeys = 64;  // of a block
   static constexpr int kChunks = D / 64;             // 128-byte columns of a row
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kStageBytes = kKeys * D * 2;
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 256 ? 5 : 10;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kSoftWarps + 2);
-  // tensor memory: two buffers of scores, then the accumulators
-  static constexpr int kScores = 128;  // columns between the buffers
+  static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 1);
+  // tensor memory: two buffers of scores for each tile, then the accumulators
+  static constexpr int kScores = kTiles == 1 ? 128 : 64;  // columns from buffer to buffer
   static constexpr int kAcc = 256;
 };
 
@@ -141,22 +143,36 @@ __device__ __forceinline__ float ex2_fast(float x) {
   return r;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A value that is the same in all lanes, told to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 template <int D>
 __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const PromptAttnArgs a) {
   using Cfg = PromptCfg<D>;
   constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages, THREADS = Cfg::kThreads;
-  constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + 1;
+  constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + NT;
   extern __shared__ __align__(1024) uint8_t prompt_smem[];
-  __shared__ __align__(8) uint64_t q_full, kv_full[ST], kv_empty[ST], s_full[2], p_full[2], o_done[2], drain;
+  __shared__ __align__(8) uint64_t q_full, kv_full[ST], kv_empty[ST], s_full[NT][2], p_full[NT][2], o_done[NT], v_raw, drain[NT];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int scan[THREADS / 32], found[2];  // sequence, tile pair within it
 
   uint8_t* smem = align_shared<1024>(prompt_smem);
   uint8_t* ring = smem + NT * Cfg::kQBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int hx = a.Hkv * a.groups;  // head groups
   const int tile = blockIdx.x / hx, hq = blockIdx.x % hx;
   const int per_tile = 128 / a.pack;  // tokens of a tile
@@ -167,14 +183,17 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     mbar_init(&q_full, 1);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], NT);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);  // the warps of a tile
+    for (int t = 0; t < NT; ++t) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[t][i], 1);
+        mbar_init(&p_full[t][i], 4);  // the warps of a tile
+      }
       mbar_init(&o_done[t], 1);
     }
-    mbar_init(&drain, 1);
+    mbar_init(&v_raw, 1);
+    for (int t = 0; t < NT; ++t) mbar_init(&drain[t], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&mapQ);
     tma_prefetch_desc(&mapK);
@@ -251,137 +270,124 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
   const uint32_t tmem = tmem_slot;
 
   if (warp == TMA_WARP) {
-    if (lane == 0 && most > 0) {
-      uint32_t bytes = 0;
+    if (most > 0) {
+      if (lane == 0) {
+        uint32_t bytes = 0;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) bytes += blocks[t] > 0 ? Cfg::kQBytes : 0;
-      mbar_arrive_expect_tx(&q_full, bytes);
+        for (int t = 0; t < NT; ++t) bytes += blocks[t] > 0 ? Cfg::kQBytes : 0;
+        mbar_arrive_expect_tx(&q_full, bytes);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (blocks[t] > 0)
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full, 64 * c, head0,
-                        q0 + first + t * per_tile);
+        for (int t = 0; t < NT; ++t)
+          if (blocks[t] > 0)
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full, 64 * c, head0,
+                          q0 + first + t * per_tile);
+      }
       RingPos pos;
       int issued = 0;
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int j) {
-        if (ok) ok = mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag);
+      auto load = [&](const CUtensorMap* map, int j, uint64_t* full) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag));
         if (!ok) return;
-        mbar_arrive_expect_tx(&kv_full[pos.s], Cfg::kStageBytes);
-        for (int c = 0; c < Cfg::kChunks; ++c)
-          tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, &kv_full[pos.s], 64 * c, hk, k0 + j * BN);
-        pos.advance(1, ST);
-        ++issued;
-      };
-      // in the order of the products below
-      load(&mapK, 0);
-      for (int j = 0; j < most; ++j) {
-        if (NT == 1) {
-          if (j + 1 < most) load(&mapK, j + 1);
-          load(&mapV, j);
-        } else {
-          load(&mapV, j);
-          if (j + 1 < most) load(&mapK, j + 1);
-        }
-      }
-      if (abort_flag) {  // no copy may still be landing when the CTA exits
-        drain_wait(&q_full, 0);
-        for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
-      }
-    }
-  } else if (warp == MMA_WARP) {
-    if (most > 0) {
-      constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
-      bool ok = mbar_wait(&q_full, 0, &abort_flag);
-      RingPos pos;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
-        tc_fence_after();
-      };
-      // scores of the tile in shared memory q against the K block in stage s
-      auto scores = [&](int q, int s, int buf) {
-        if (lane != 0 || !ok) return;
-        const uint64_t qd = smem_desc_sw128(smem_u32(smem + q * Cfg::kQBytes));
-        const uint64_t kd = smem_desc_sw128(smem_u32(ring + s * Cfg::kStageBytes));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16_ss(tmem + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
-                      kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
-        mma_commit(&s_full[buf]);
-      };
-      auto weigh = [&](int t, int s, int buf, bool acc) {
-        if (lane != 0 || !ok) return;
-        const uint64_t vd = smem_desc_sw128_mn(smem_u32(ring + s * Cfg::kStageBytes), BN * 128);
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_bf16_ts(tmem + Cfg::kAcc + t * D, tmem + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o,
-                      acc || k > 0);
-        mma_commit(&o_done[t]);
-      };
-      auto release = [&](int s) {
-        if (lane == 0 && ok) mma_commit(&kv_empty[s]);
-      };
-      // waits for the V block j in the ring's next stage and clears its rows behind the last key
-      auto take_v = [&](int j) {
-        wait(&kv_full[pos.s], pos.ph);
-        if (ok && (j + 1) * BN > nk) {
-          const int keep = nk - j * BN;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, Cfg::kStageBytes);
           for (int c = 0; c < Cfg::kChunks; ++c)
-            for (int x = keep * 8 + lane; x < BN * 8; x += 32)
+            tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, full, 64 * c, hk, k0 + j * BN);
+        }
+        if (full == &v_raw) {  // the last block, with rows that are no keys of the sequence
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, 0, &abort_flag));
+          if (!ok) return;
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            for (int x = (nk - j * BN) * 8 + lane; x < BN * 8; x += 32)
               reinterpret_cast<uint4*>(ring + pos.s * Cfg::kStageBytes + c * (BN * 128))[x] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_shared();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[pos.s]);
         }
+        pos.advance(1, ST);
+        ++issued;
       };
-      wait(&kv_full[pos.s], pos.ph);
-      if constexpr (NT == 2) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (blocks[t] > 0) scores(t, pos.s, t);
-        release(pos.s);
-        pos.advance(1, ST);
-        for (int j = 0; j < most && ok; ++j) {
-          take_v(j);
-          const int vs = pos.s;
-          pos.advance(1, ST);
-          const bool next = j + 1 < most;
-          if (next) wait(&kv_full[pos.s], pos.ph);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (j < blocks[t]) {
-              wait(&p_full[t], (uint32_t)j & 1u);
-              weigh(t, vs, t, j > 0);
-            }
-            if (t == NT - 1) release(vs);
-            if (j + 1 < blocks[t]) scores(t, pos.s, t);
-          }
-          if (next) {
-            release(pos.s);
-            pos.advance(1, ST);
-          }
-        }
-      } else {
-        scores(0, pos.s, 0);
-        release(pos.s);
-        pos.advance(1, ST);
-        for (int j = 0; j < most && ok; ++j) {
-          if (j + 1 < most) {
-            wait(&kv_full[pos.s], pos.ph);
-            scores(0, pos.s, (j + 1) & 1);
-            release(pos.s);
-            pos.advance(1, ST);
-          }
-          take_v(j);
-          wait(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
-          weigh(0, pos.s, j & 1, j > 0);
-          release(pos.s);
-          pos.advance(1, ST);
-        }
+      auto load_k = [&](int j) { load(&mapK, j, &kv_full[pos.s]); };
+      auto load_v = [&](int j) { load(&mapV, j, (j + 1) * BN > nk ? &v_raw : &kv_full[pos.s]); };
+      // in the order of the products below
+      load_k(0);
+      for (int j = 0; j < most; ++j) {
+        if (j + 1 < most) load_k(j + 1);
+        load_v(j);
       }
+      if (abort_flag) {  // no copy may still be landing when the CTA exits
+        drain_wait(&q_full, 0);
+        drain_wait(&v_raw, 0);
+        for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
+      }
+    }
+  } else if (warp >= MMA_WARP) {
+    if (most > 0) {
+      const int t = warp - MMA_WARP, n = uniform(t == 0 ? blocks[0] : blocks[NT - 1]), last = uniform(most);
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
+      constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem + t * Cfg::kQBytes));
+      const uint64_t kd0 = smem_desc_sw128(smem_u32(ring));
+      const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(ring), BN * 128);
+      const uint32_t t_acc = tm + Cfg::kAcc + t * D;
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&q_full, 0, &abort_flag));
+      RingPos pos;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+      };
+      const uint32_t t_s = tm + 2 * t * Cfg::kScores;
+      auto scores = [&](int buf) {  // against the K block in the ring's current stage
+        const uint64_t kd = kd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
+        if (!elect_one()) return;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16_ss(t_s + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
+                      kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
+        mma_commit(&s_full[t][buf]);
+      };
+      auto weigh = [&](int buf, uint32_t acc) {  // with the V block in the ring's current stage
+        const uint64_t vd = vd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
+        if (!elect_one()) return;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_bf16_ts(t_acc, t_s + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o, k > 0 ? 1u : acc);
+        mma_commit(&o_done[t]);
+      };
+      auto release = [&]() {  // the ring's current stage, once the products so far are done
+        if (ok && elect_one()) mma_commit(&kv_empty[pos.s]);
+        pos.advance(1, ST);
+      };
+      auto skip = [&]() {  // a block that only the other tile sees
+        wait(&kv_full[pos.s], pos.ph);
+        if (ok && lane == 0) mbar_arrive(&kv_empty[pos.s]);
+        pos.advance(1, ST);
+      };
+      // K 0, then K j + 1 and V j in turn: the next scores come before this block's weights are ready
+      if (n > 0) {
+        wait(&kv_full[pos.s], pos.ph);
+        if (ok) scores(0);
+        release();
+        for (int j = 0; j < n - 1 && ok; ++j) {
+          wait(&kv_full[pos.s], pos.ph);
+          if (ok) scores((j + 1) & 1);
+          release();
+          wait(&kv_full[pos.s], pos.ph);
+          wait(&p_full[t][j & 1], (uint32_t)(j >> 1) & 1u);
+          tc_fence_after();
+          if (ok) weigh(j & 1, j > 0);
+          release();
+        }
+        if (n < last) skip();
+        wait(&kv_full[pos.s], pos.ph);
+        wait(&p_full[t][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u);
+        tc_fence_after();
+        if (ok) weigh((n - 1) & 1, n > 1);
+        release();
+      }
+      for (int x = n > 0 ? 2 * n + (n < last ? 1 : 0) : 0; x < 2 * last && ok; ++x) skip();
       if (!ok && lane == 0) {  // no product may still be running when the CTA exits
-        mma_commit(&drain);
-        drain_wait(&drain, 0);
+        mma_commit(&drain[t]);
+        drain_wait(&drain[t], 0);
       }
     }
   } else {
@@ -391,23 +397,26 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_acc = tmem + lanes + Cfg::kAcc + t * D;
     const int token = first + t * per_tile + row / a.pack, head = head0 + row % a.pack;
-    const int n = blocks[NT == 1 ? 0 : t];
+    const int n = t == 0 ? blocks[0] : blocks[NT - 1];
     const int visible = seen(token);
     const int unmasked = seen(first + t * per_tile);  // keys that every row of the tile sees
     const float sl2 = a.scale_log2;
     const float slack = 8.f / sl2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int buf = NT == 1 ? j & 1 : t;
-      ok = mbar_wait(&s_full[buf], (uint32_t)(NT == 1 ? j >> 1 : j) & 1u, &abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+    float s[BN];
+    // the block's scores, once they are there; asynchronous: tmem_ld_wait
+    auto fetch = [&](int j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t][j & 1], (uint32_t)(j >> 1) & 1u, &abort_flag));
+      if (!ok) return;
       tc_fence_after();
-      const uint32_t t_s = tmem + lanes + buf * Cfg::kScores;
-      float s[BN];
+      const uint32_t t_s = tmem + lanes + (2 * t + (j & 1)) * Cfg::kScores;
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tmem_ld_nowait_x32(t_s + c, s + c);
+    };
+    if (n > 0) fetch(0);
+    for (int j = 0; j < n && ok; ++j) {
+      const uint32_t t_s = tmem + lanes + (2 * t + (j & 1)) * Cfg::kScores;
       tmem_ld_wait(s);
       if (a.sign != 1.f) {
 #pragma unroll
@@ -433,12 +442,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         const float f = up ? ex2_fast((m - mn) * sl2) : 1.f;
         m = mn;
         l *= f;
-        if (NT == 1) {  // with two tiles the products before these scores are known to be complete
-          ok = mbar_wait(&o_done[0], (uint32_t)(j - 1) & 1u, &abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        // the accumulator must hold the block before this one (these scores tell of the one before that)
+        ok = mbar_wait(&o_done[t], (uint32_t)(j - 1) & 1u, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -450,28 +458,31 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         }
       }
       const float shift = m == -INFINITY ? 0.f : -m * sl2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const F2 sl22(sl2, sl2), shift2(shift, shift);
+      F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+      uint32_t p[BN / 2];
 #pragma unroll
-      for (int c = 0; c < BN; c += 64) {
-        uint32_t p[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2_fast(fmaf(s[c + 2 * i], sl2, shift)), p1 = ex2_fast(fmaf(s[c + 2 * i + 1], sl2, shift));
-          sum[2 * (i & 1)] += p0;
-          sum[2 * (i & 1) + 1] += p1;
-          p[i] = pack_bf16(p0, p1);
-        }
-        tmem_st_32x32b_x32(t_s + c / 2, p);
+      for (int i = 0; i < BN / 2; ++i) {
+        float p0, p1;
+        fma2(F2(s[2 * i], s[2 * i + 1]), sl22, shift2).split(p0, p1);
+        p0 = ex2_fast(p0);
+        p1 = ex2_fast(p1);
+        sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
+        p[i] = pack_bf16(p0, p1);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_32x32b_x32(t_s, p);
+      if (j + 1 < n) fetch(j + 1);  // under the store
+      float l0, l1;
+      add2(sum[0], sum[1]).split(l0, l1);
+      l += l0 + l1;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[buf]);
+      if (lane == 0) mbar_arrive(&p_full[t][j & 1]);
     }
     if (ok && n > 0) {
-      // one phase at a time: with one tile the last scores only tell that the products of block n - 3 are done
-      if (NT == 1 && n > 1) mbar_wait(&o_done[t], (uint32_t)(n - 2) & 1u, &abort_flag);
+      // one phase at a time: the last scores only tell that the products of block n - 3 are done
+      if (n > 1) mbar_wait(&o_done[t], (uint32_t)(n - 2) & 1u, &abort_flag);
       ok = mbar_wait(&o_done[t], (uint32_t)(n - 1) & 1u, &abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
