@@ -27,8 +27,13 @@
 //                    last key, which may hold anything, are cleared in shared memory (the scores of such
 //                    keys are replaced by -inf)
 //
-// One CTA per SM; a launch has a CTA per (tile pair, head group), the pairs of most keys first. Sizes of
-// sequences are read on the device: a CTA finds its tile from the borders.
+//   a scheduling warp
+//
+// One CTA per SM. The grid has a CTA per (tile pair, head group), the pairs of most keys of a sequence
+// first, but a running CTA takes the places of those that have not started yet (cluster launch control), so
+// that the copies of the next pair's Q and its first scores run under the softmax and the output of this one.
+// (A CTA for each pair took 9 to 11 us of start and end.) Sizes of sequences are read on the device: the
+// scheduling warp finds a pair's sequence from the borders.
 #pragma once
 
 #include <cuda.h>
@@ -77,7 +82,7 @@ struct PromptCfg {
   static constexpr int kStages = D == 256 ? 5 : 10;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 1);
+  static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 2);
   // tensor memory: two buffers of scores for each tile, then the accumulators
   static constexpr int kScores = kTiles == 1 ? 128 : 64;  // columns from buffer to buffer
   static constexpr int kAcc = 256;
@@ -157,135 +162,206 @@ __device__ __forceinline__ bool elect_one() {
 // A value that is the same in all lanes, told to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// Cluster launch control: takes the place of a CTA of this grid that has not started (16 bytes of answer,
+// counted on `bar`).
+__device__ __forceinline__ void cancel_next(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(smem_u32(answer)), "r"(smem_u32(bar))
+               : "memory");
+}
+// The number of the CTA whose place was taken, or -1 if there was none left.
+__device__ __forceinline__ int cancelled_cta(const void* answer) {
+  uint32_t x, ok;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x), "=r"(ok)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+// A tile pair of a sequence and a head group, as the scheduling warp hands it out.
+struct PromptItem {
+  int first;  // first token of the sequence; negative: no more
+  int hq;     // head group
+  int q0, nq, k0, nk;
+  int pad[2];
+};
+
 template <int D>
 __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const PromptAttnArgs a) {
   using Cfg = PromptCfg<D>;
-  constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages, THREADS = Cfg::kThreads;
-  constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + NT;
+  constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages;
+  constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + NT, PLAN_WARP = TMA_WARP + 1;
   extern __shared__ __align__(1024) uint8_t prompt_smem[];
-  __shared__ __align__(8) uint64_t q_full, kv_full[ST], kv_empty[ST], s_full[NT][2], p_full[NT][2], o_done[NT], v_raw, drain[NT];
+  __shared__ __align__(8) uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT][2], p_full[NT][2],
+      o_done[NT][2], v_raw, drain[NT], item_full[2], item_empty[2], answer_full;
+  __shared__ __align__(16) uint8_t answer[16];
+  __shared__ __align__(16) PromptItem items[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ int scan[THREADS / 32], found[2];  // sequence, tile pair within it
 
   uint8_t* smem = align_shared<1024>(prompt_smem);
   uint8_t* ring = smem + NT * Cfg::kQBytes;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int hx = a.Hkv * a.groups;  // head groups
-  const int tile = blockIdx.x / hx, hq = blockIdx.x % hx;
-  const int per_tile = 128 / a.pack;  // tokens of a tile
+  const int hx = a.Hkv * a.groups;      // head groups
+  const int per_tile = 128 / a.pack;    // tokens of a tile
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    found[0] = -1;
-    mbar_init(&q_full, 1);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], NT);
     }
     for (int t = 0; t < NT; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[t][i], 1);
         mbar_init(&p_full[t][i], 4);  // the warps of a tile
+        mbar_init(&o_done[t][i], 1);
       }
-      mbar_init(&o_done[t], 1);
+      mbar_init(&drain[t], 1);
     }
     mbar_init(&v_raw, 1);
-    for (int t = 0; t < NT; ++t) mbar_init(&drain[t], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], PLAN_WARP);  // every other warp reads it
+    }
+    mbar_init(&answer_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&mapQ);
     tma_prefetch_desc(&mapK);
     tma_prefetch_desc(&mapV);
   }
-  pdl_wait();
-  pdl_launch_dependents();
-
-  // ---- which tile pair: a thread counts those of a run of consecutive sequences
-  {
-    const int run = (a.B + THREADS - 1) / THREADS;
-    const int b_lo = threadIdx.x * run, b_hi = b_lo + run < a.B ? b_lo + run : a.B;
-    int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      int q0, nq, k0, nk;
-      const bool good = prompt_borders(a, b, q0, nq, k0, nk);
-      if (blockIdx.x == 0 && (!good || nq > a.max_q)) raise_error(kErrBadIndex);
-      if (good) mine += ((nq < a.max_q ? nq : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
-    }
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w)
-      if (w < warp) upto += scan[w];
-    int at = upto - mine;
-    if (tile >= at && tile < upto) {
-      for (int b = b_lo; b < b_hi; ++b) {
-        int q0, nq, k0, nk;
-        if (!prompt_borders(a, b, q0, nq, k0, nk)) continue;
-        const int n = ((nq < a.max_q ? nq : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
-        if (tile < at + n) {
-          found[0] = b;
-          found[1] = n - 1 - (tile - at);  // the last tokens see most keys
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-  }
-  const int b = found[0];
-  if (b < 0) return;  // fewer tiles than the grid has room for
-  int q0, nq_all, k0, nk;
-  prompt_borders(a, b, q0, nq_all, k0, nk);
-  const int nq = nq_all < a.max_q ? nq_all : a.max_q;
-  const int first = found[1] * NT * per_tile;  // token of the sequence
-  const int hk = hq / a.groups, head0 = hk * (a.Hq / a.Hkv) + hq % a.groups * a.pack;
-  auto seen = [&](int token) {
-    const int n = a.causal ? token + 1 + nk - nq_all : nk;
-    return n < 0 ? 0 : n > nk ? nk : n;
-  };
-  int blocks[NT], most = 0;  // key blocks that a tile sees
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int lo = first + t * per_tile, hi = lo + per_tile < nq ? lo + per_tile : nq;
-    blocks[t] = lo < nq ? (seen(hi - 1) + BN - 1) / BN : 0;
-    most = blocks[t] > most ? blocks[t] : most;
-  }
-
   if (warp == MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == TMA_WARP) {
-    if (most > 0) {
-      if (lane == 0) {
-        uint32_t bytes = 0;
+  // ---- the item that the scheduling warp hands out next, the same to every other warp
+  bool ok = true;
+  int first = 0, q0 = 0, nq_all = 0, nq = 0, k0 = 0, nk = 0, hk = 0, head0 = 0, most = 0, blocks[NT];
+  RingPos item_pos;
+  auto seen = [&](int token) {
+    const int n = a.causal ? token + 1 + nk - nq_all : nk;
+    return n < 0 ? 0 : n > nk ? nk : n;
+  };
+  auto next_item = [&]() {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&item_full[item_pos.s], item_pos.ph, &abort_flag));
+    if (!ok) return false;
+    const PromptItem& it = items[item_pos.s];
+    first = uniform(it.first);
+    q0 = uniform(it.q0);
+    nq_all = uniform(it.nq);
+    k0 = uniform(it.k0);
+    nk = uniform(it.nk);
+    const int hq = uniform(it.hq);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[item_pos.s]);
+    item_pos.advance(1, 2);
+    if (first < 0) return false;
+    nq = nq_all < a.max_q ? nq_all : a.max_q;
+    hk = hq / a.groups;
+    head0 = hk * (a.Hq / a.Hkv) + hq % a.groups * a.pack;
+    most = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) bytes += blocks[t] > 0 ? Cfg::kQBytes : 0;
-        mbar_arrive_expect_tx(&q_full, bytes);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (blocks[t] > 0)
-            for (int c = 0; c < Cfg::kChunks; ++c)
-              tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full, 64 * c, head0,
-                          q0 + first + t * per_tile);
+    for (int t = 0; t < NT; ++t) {  // key blocks that a tile sees
+      const int lo = first + t * per_tile, hi = lo + per_tile < nq ? lo + per_tile : nq;
+      blocks[t] = lo < nq ? (seen(hi - 1) + BN - 1) / BN : 0;
+      most = blocks[t] > most ? blocks[t] : most;
+    }
+    return true;
+  };
+
+  if (warp == PLAN_WARP) {
+    // ---- a CTA number's tile pair: the borders are passed 32 sequences at a time, from where the last
+    // search ended (numbers mostly rise)
+    int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32
+    int cta = blockIdx.x;
+    uint32_t answers = 0;
+    bool more = true;
+    while (more) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[item_pos.s], item_pos.ph ^ 1u, &abort_flag));
+      if (!ok) break;
+      if (cta < 0) {  // not the first item
+        if (lane == 0) {
+          fence_proxy_async_shared();
+          mbar_arrive_expect_tx(&answer_full, 16);
+          cancel_next(answer, &answer_full);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&answer_full, answers & 1u, &abort_flag));
+        ++answers;
+        if (!ok) {
+          drain_wait(&answer_full, (answers - 1) & 1u);
+          break;
+        }
+        cta = cancelled_cta(answer);
       }
-      RingPos pos;
-      int issued = 0;
-      bool ok = true;
+      PromptItem it = {-1, 0, 0, 0, 0, 0, {0, 0}};
+      if (cta == 0)
+        for (int b = lane; b < a.B; b += 32) {
+          int q, n, k, m;
+          if (!prompt_borders(a, b, q, n, k, m) || n > a.max_q) raise_error(kErrBadIndex);
+        }
+      if (cta >= 0) {
+        const int tile = cta / hx;
+        it.hq = cta % hx;
+        if (tile < base_tiles) base_b = base_tiles = 0;
+        while (base_b < a.B) {
+          const int b = base_b + lane;
+          int q, n = 0, k = 0, m = 0, tiles = 0;
+          if (b < a.B && prompt_borders(a, b, q, n, k, m))
+            tiles = ((n < a.max_q ? n : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
+          int upto = tiles;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const int rank = tile - base_tiles;
+          const uint32_t here = __ballot_sync(0xffffffffu, rank < upto);
+          if (here != 0u) {  // the first sequence that reaches the rank; its last tokens see most keys
+            const int src = __ffs(here) - 1;
+            it.first = __shfl_sync(0xffffffffu, (upto - 1 - rank) * NT * per_tile, src);
+            it.q0 = __shfl_sync(0xffffffffu, q, src);
+            it.nq = __shfl_sync(0xffffffffu, n, src);
+            it.k0 = __shfl_sync(0xffffffffu, k, src);
+            it.nk = __shfl_sync(0xffffffffu, m, src);
+            break;
+          }
+          base_tiles += __shfl_sync(0xffffffffu, upto, 31);
+          base_b += 32;
+        }
+      }
+      more = it.first >= 0;
+      if (lane == 0) {
+        items[item_pos.s] = it;
+        mbar_arrive(&item_full[item_pos.s]);
+      }
+      item_pos.advance(1, 2);
+      cta = -1;
+    }
+  } else if (warp == TMA_WARP) {
+    RingPos pos;
+    int issued = 0;
+    uint32_t raws = 0, count[NT];  // copies on v_raw and q_full
+#pragma unroll
+    for (int t = 0; t < NT; ++t) count[t] = 0;
+    while (next_item()) {
       auto load = [&](const CUtensorMap* map, int j, uint64_t* full) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag));
         if (!ok) return;
@@ -295,7 +371,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, full, 64 * c, hk, k0 + j * BN);
         }
         if (full == &v_raw) {  // the last block, with rows that are no keys of the sequence
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, 0, &abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raws & 1u, &abort_flag));
+          ++raws;
           if (!ok) return;
           for (int c = 0; c < Cfg::kChunks; ++c)
             for (int x = (nk - j * BN) * 8 + lane; x < BN * 8; x += 32)
@@ -307,88 +384,111 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         pos.advance(1, ST);
         ++issued;
       };
+      auto load_q = [&](int t) {
+        if (blocks[t] == 0) return;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[t], (count[t] & 1u) ^ 1u, &abort_flag));
+        if (!ok) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[t], Cfg::kQBytes);
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full[t], 64 * c, head0,
+                        q0 + first + t * per_tile);
+        }
+        ++count[t];
+      };
       auto load_k = [&](int j) { load(&mapK, j, &kv_full[pos.s]); };
       auto load_v = [&](int j) { load(&mapV, j, (j + 1) * BN > nk ? &v_raw : &kv_full[pos.s]); };
-      // in the order of the products below
-      load_k(0);
-      for (int j = 0; j < most; ++j) {
+      // in the order of the products below; the first K goes ahead, since its stage is free early
+      if (most > 0) load_k(0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) load_q(t);
+      for (int j = 0; j < most && ok; ++j) {
         if (j + 1 < most) load_k(j + 1);
         load_v(j);
       }
-      if (abort_flag) {  // no copy may still be landing when the CTA exits
-        drain_wait(&q_full, 0);
-        drain_wait(&v_raw, 0);
-        for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
-      }
+      if (!ok) break;
+    }
+    if (abort_flag) {  // no copy may still be landing when the CTA exits
+      for (int t = 0; t < NT; ++t)
+        if (count[t] > 0) drain_wait(&q_full[t], (count[t] - 1) & 1u);
+      drain_wait(&v_raw, raws & 1u);
+      for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
     }
   } else if (warp >= MMA_WARP) {
-    if (most > 0) {
-      const int t = warp - MMA_WARP, n = uniform(t == 0 ? blocks[0] : blocks[NT - 1]), last = uniform(most);
-      const uint32_t tm = (uint32_t)uniform((int)tmem);
-      constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
-      const uint64_t qd = smem_desc_sw128(smem_u32(smem + t * Cfg::kQBytes));
-      const uint64_t kd0 = smem_desc_sw128(smem_u32(ring));
-      const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(ring), BN * 128);
-      const uint32_t t_acc = tm + Cfg::kAcc + t * D;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&q_full, 0, &abort_flag));
-      RingPos pos;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
-      };
-      const uint32_t t_s = tm + 2 * t * Cfg::kScores;
-      auto scores = [&](int buf) {  // against the K block in the ring's current stage
-        const uint64_t kd = kd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
-        if (!elect_one()) return;
+    const int t = warp - MMA_WARP;
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
+    const uint64_t qd = smem_desc_sw128(smem_u32(smem + t * Cfg::kQBytes));
+    const uint64_t kd0 = smem_desc_sw128(smem_u32(ring));
+    const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(ring), BN * 128);
+    const uint32_t t_acc = tm + Cfg::kAcc + t * D, t_s = tm + 2 * t * Cfg::kScores;
+    RingPos pos;
+    uint32_t done = 0, queries = 0;  // key blocks of this tile so far, copies of its Q
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+    };
+    auto scores = [&](uint32_t buf) {  // against the K block in the ring's current stage
+      const uint64_t kd = kd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
+      if (!elect_one()) return;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_bf16_ss(t_s + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
-                      kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
-        mma_commit(&s_full[t][buf]);
-      };
-      auto weigh = [&](int buf, uint32_t acc) {  // with the V block in the ring's current stage
-        const uint64_t vd = vd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
-        if (!elect_one()) return;
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16_ss(t_s + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
+                    kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
+      mma_commit(&s_full[t][buf]);
+    };
+    auto weigh = [&](uint32_t buf, uint32_t acc) {  // with the V block in the ring's current stage
+      const uint64_t vd = vd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
+      if (!elect_one()) return;
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_bf16_ts(t_acc, t_s + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o, k > 0 ? 1u : acc);
-        mma_commit(&o_done[t]);
-      };
-      auto release = [&]() {  // the ring's current stage, once the products so far are done
-        if (ok && elect_one()) mma_commit(&kv_empty[pos.s]);
-        pos.advance(1, ST);
-      };
-      auto skip = [&]() {  // a block that only the other tile sees
-        wait(&kv_full[pos.s], pos.ph);
-        if (ok && lane == 0) mbar_arrive(&kv_empty[pos.s]);
-        pos.advance(1, ST);
-      };
-      // K 0, then K j + 1 and V j in turn: the next scores come before this block's weights are ready
+      for (int k = 0; k < BN / 16; ++k)
+        mma_bf16_ts(t_acc, t_s + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o, k > 0 ? 1u : acc);
+      mma_commit(&o_done[t][buf]);
+    };
+    auto release = [&]() {  // the ring's current stage, once the products so far are done
+      if (ok && elect_one()) mma_commit(&kv_empty[pos.s]);
+      pos.advance(1, ST);
+    };
+    auto skip = [&]() {  // a block that only the other tile sees
+      wait(&kv_full[pos.s], pos.ph);
+      if (ok && lane == 0) mbar_arrive(&kv_empty[pos.s]);
+      pos.advance(1, ST);
+    };
+    while (next_item()) {
+      const int n = t == 0 ? blocks[0] : blocks[NT - 1], last = most;
+      // K 0, then K j + 1 and V j in turn: the next scores come before this block's weights are ready.
+      // The accumulator is free when the first weights are there, which come after the last output.
       if (n > 0) {
+        wait(&q_full[t], queries & 1u);
+        ++queries;
         wait(&kv_full[pos.s], pos.ph);
-        if (ok) scores(0);
+        if (ok) scores(done & 1u);
         release();
-        for (int j = 0; j < n - 1 && ok; ++j) {
+        for (int j = 0; j < n - 1 && ok; ++j, ++done) {
           wait(&kv_full[pos.s], pos.ph);
-          if (ok) scores((j + 1) & 1);
+          if (ok) scores((done + 1) & 1u);
+          if (j == n - 2 && ok && elect_one()) mma_commit(&q_empty[t]);
           release();
           wait(&kv_full[pos.s], pos.ph);
-          wait(&p_full[t][j & 1], (uint32_t)(j >> 1) & 1u);
+          wait(&p_full[t][done & 1u], (done >> 1) & 1u);
           tc_fence_after();
-          if (ok) weigh(j & 1, j > 0);
+          if (ok) weigh(done & 1u, j > 0);
           release();
         }
+        if (n == 1 && ok && elect_one()) mma_commit(&q_empty[t]);
         if (n < last) skip();
         wait(&kv_full[pos.s], pos.ph);
-        wait(&p_full[t][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u);
+        wait(&p_full[t][done & 1u], (done >> 1) & 1u);
         tc_fence_after();
-        if (ok) weigh((n - 1) & 1, n > 1);
+        if (ok) weigh(done & 1u, n > 1);
         release();
+        ++done;
       }
       for (int x = n > 0 ? 2 * n + (n < last ? 1 : 0) : 0; x < 2 * last && ok; ++x) skip();
-      if (!ok && lane == 0) {  // no product may still be running when the CTA exits
-        mma_commit(&drain[t]);
-        drain_wait(&drain[t], 0);
-      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) {  // no product may still be running when the CTA exits
+      mma_commit(&drain[t]);
+      drain_wait(&drain[t], 0);
     }
   } else {
     // ---- softmax: a thread per row
@@ -396,121 +496,124 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_acc = tmem + lanes + Cfg::kAcc + t * D;
-    const int token = first + t * per_tile + row / a.pack, head = head0 + row % a.pack;
-    const int n = t == 0 ? blocks[0] : blocks[NT - 1];
-    const int visible = seen(token);
-    const int unmasked = seen(first + t * per_tile);  // keys that every row of the tile sees
     const float sl2 = a.scale_log2;
     const float slack = 8.f / sl2;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    float s[BN];
-    // the block's scores, once they are there; asynchronous: tmem_ld_wait
-    auto fetch = [&](int j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t][j & 1], (uint32_t)(j >> 1) & 1u, &abort_flag));
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t t_s = tmem + lanes + (2 * t + (j & 1)) * Cfg::kScores;
-#pragma unroll
-      for (int c = 0; c < BN; c += 32) tmem_ld_nowait_x32(t_s + c, s + c);
-    };
-    if (n > 0) fetch(0);
-    for (int j = 0; j < n && ok; ++j) {
-      const uint32_t t_s = tmem + lanes + (2 * t + (j & 1)) * Cfg::kScores;
-      tmem_ld_wait(s);
-      if (a.sign != 1.f) {
-#pragma unroll
-        for (int c = 0; c < BN; ++c) s[c] *= a.sign;
-      }
-      if ((j + 1) * BN > unmasked) {
-        const int lim = visible - j * BN;
-#pragma unroll
-        for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < BN; c += 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = c + 4 + i < BN ? fmaxf(fmaxf(mx[i], s[c + i]), s[c + 4 + i]) : fmaxf(mx[i], s[c + i]);
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool up = top > m + slack;
-      if (j == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, up)) {
-        const float mn = up ? top : m;
-        const float f = up ? ex2_fast((m - mn) * sl2) : 1.f;
-        m = mn;
-        l *= f;
-        // the accumulator must hold the block before this one (these scores tell of the one before that)
-        ok = mbar_wait(&o_done[t], (uint32_t)(j - 1) & 1u, &abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+    uint32_t done = 0;  // key blocks of this tile so far
+    while (next_item()) {
+      const int token = first + t * per_tile + row / a.pack, head = head0 + row % a.pack;
+      const int n = t == 0 ? blocks[0] : blocks[NT - 1];
+      const int visible = seen(token);
+      const int unmasked = seen(first + t * per_tile);  // keys that every row of the tile sees
+      float m = -INFINITY, l = 0.f;
+      float s[BN];
+      // the scores of the block number x, once they are there; asynchronous: tmem_ld_wait
+      auto fetch = [&](uint32_t x) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t][x & 1u], (x >> 1) & 1u, &abort_flag));
+        if (!ok) return;
         tc_fence_after();
+        const uint32_t t_s = tmem + lanes + (2 * t + (x & 1u)) * Cfg::kScores;
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) tmem_ld_nowait_x32(t_s + c, s + c);
+      };
+      if (n > 0) fetch(done);
+      for (int j = 0; j < n && ok; ++j, ++done) {
+        const uint32_t t_s = tmem + lanes + (2 * t + (done & 1u)) * Cfg::kScores;
+        tmem_ld_wait(s);
+        if (a.sign != 1.f) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] *= a.sign;
+        }
+        if ((j + 1) * BN > unmasked) {
+          const int lim = visible - j * BN;
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < BN; c += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = c + 4 + i < BN ? fmaxf(fmaxf(mx[i], s[c + i]), s[c + 4 + i]) : fmaxf(mx[i], s[c + i]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool up = top > m + slack;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, up)) {
+          const float mn = up ? top : m;
+          const float f = up ? ex2_fast((m - mn) * sl2) : 1.f;
+          m = mn;
+          l *= f;
+          // the accumulator must hold the block before this one. (A barrier for even and one for odd blocks:
+          // these scores tell that the block before that is done, and the next one waits for these weights,
+          // so that neither an older nor a newer phase can be taken for it.)
+          ok = mbar_wait(&o_done[t][(done - 1) & 1u], ((done - 1) >> 1) & 1u, &abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld_nowait_x32(t_acc + c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st_32x32b_x32(t_acc + c, reinterpret_cast<const uint32_t(&)[32]>(o));
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : -m * sl2;
+        const F2 sl22(sl2, sl2), shift2(shift, shift);
+        F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+        uint32_t p[BN / 2];
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) {
+          float p0, p1;
+          fma2(F2(s[2 * i], s[2 * i + 1]), sl22, shift2).split(p0, p1);
+          p0 = ex2_fast(p0);
+          p1 = ex2_fast(p1);
+          sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
+          p[i] = pack_bf16(p0, p1);
+        }
+        tmem_st_32x32b_x32(t_s, p);
+        if (j + 1 < n) fetch(done + 1);  // under the store
+        float l0, l1;
+        add2(sum[0], sum[1]).split(l0, l1);
+        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][done & 1u]);
+      }
+      if (ok && n > 0) {
+        ok = mbar_wait(&o_done[t][(done - 1) & 1u], ((done - 1) >> 1) & 1u, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      const bool store = ok && token < nq;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const size_t ih = (size_t)(q0 + token) * a.Hq + head;
+      if (store && a.lse) a.lse[ih] = l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      if (ok) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          tmem_ld_nowait_x32(t_acc + c, o);
-          tmem_ld_wait(o);
+          if (n > 0) {
+            tmem_ld_nowait_x32(t_acc + c, o);
+            tmem_ld_wait(o);
+          }
+          if (store) {
+            uint4* dst = reinterpret_cast<uint4*>(a.O + ih * D + c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= f;
-          tmem_st_32x32b_x32(t_acc + c, reinterpret_cast<const uint32_t(&)[32]>(o));
-        }
-      }
-      const float shift = m == -INFINITY ? 0.f : -m * sl2;
-      const F2 sl22(sl2, sl2), shift2(shift, shift);
-      F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-      uint32_t p[BN / 2];
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < BN / 2; ++i) {
-        float p0, p1;
-        fma2(F2(s[2 * i], s[2 * i + 1]), sl22, shift2).split(p0, p1);
-        p0 = ex2_fast(p0);
-        p1 = ex2_fast(p1);
-        sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
-        p[i] = pack_bf16(p0, p1);
-      }
-      tmem_st_32x32b_x32(t_s, p);
-      if (j + 1 < n) fetch(j + 1);  // under the store
-      float l0, l1;
-      add2(sum[0], sum[1]).split(l0, l1);
-      l += l0 + l1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t][j & 1]);
-    }
-    if (ok && n > 0) {
-      // one phase at a time: the last scores only tell that the products of block n - 3 are done
-      if (n > 1) mbar_wait(&o_done[t], (uint32_t)(n - 2) & 1u, &abort_flag);
-      ok = mbar_wait(&o_done[t], (uint32_t)(n - 1) & 1u, &abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    const bool store = ok && token < nq;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t ih = (size_t)(q0 + token) * a.Hq + head;
-    if (store && a.lse) a.lse[ih] = l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-    if (ok) {
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        if (n > 0) {
-          tmem_ld_nowait_x32(t_acc + c, o);
-          tmem_ld_wait(o);
-        }
-        if (store) {
-          uint4* dst = reinterpret_cast<uint4*>(a.O + ih * D + c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = inv > 0.f ? pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 4; ++e)
+                w[e] = inv > 0.f ? pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
       }
+      if (!ok) break;
     }
   }
   tc_fence_before();
