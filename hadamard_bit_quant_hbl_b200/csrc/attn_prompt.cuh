@@ -11,8 +11,8 @@
 // two divides their number, so that few tokens fill it too. A CTA holds two tiles of neighbouring tokens
 // (one for 256 features, whose accumulator takes half of tensor memory) and passes the key blocks once:
 //
-//   S = Q K^T      tcgen05.mma, both operands in shared memory, 128 columns of tensor memory
-//   P = exp2(scale log2(e) (S - m)), rounded to bf16 over the same columns; sums in fp32 before rounding
+//   S = Q K^T      tcgen05.mma, both operands in shared memory, 64 keys in 64 columns of tensor memory
+//   P = exp2(scale log2(e) (S - m)), rounded to bf16, in two buffers of 32 columns; fp32 sums before rounding
 //   O += P V       tcgen05.mma, P from tensor memory, V as it lies (its features contiguous)
 //
 // The running maximum m moves only when a row's scores pass it by more than 8 binades of the weights
@@ -75,17 +75,24 @@ __device__ __forceinline__ bool prompt_borders(const PromptAttnArgs& a, int b, i
 template <int D>
 struct PromptCfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;
-  static constexpr int kKeys = 64;  // of a block
+  // Keys of a block. A product of 128 rows reads its rows of Q in 64 clocks whatever its columns, so 128
+  // keys take no longer than 64; for 256 features shared memory has no room for them.
+  static constexpr int kKeys = D == 256 ? 64 : 128;
+  static constexpr int kParts = kKeys / 64;
   static constexpr int kChunks = D / 64;             // 128-byte columns of a row
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kStageBytes = kKeys * D * 2;
-  static constexpr int kStages = D == 256 ? 5 : 10;
+  static constexpr int kStages = D == 64 ? 10 : 5;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 2);
-  // tensor memory: two buffers of scores for each tile, then the accumulators
-  static constexpr int kScores = kTiles == 1 ? 128 : 64;  // columns from buffer to buffer
-  static constexpr int kAcc = 256;
+  // Tensor memory, 512 columns: each tile's scores and weights, then the accumulators. With 128 features
+  // the weights take the scores' place, and the next scores wait until they have been used; elsewhere the
+  // next scores come as soon as these have been read (two buffers of weights for blocks of 64 keys).
+  static constexpr bool kOver = D == 128;
+  static constexpr int kBuffers = D == 256 ? 2 : 1;
+  static constexpr int kTileCols = kOver ? 128 : 192, kWeights = kOver ? 0 : D == 64 ? 128 : 64;
+  static constexpr int kAcc = D == 64 ? 384 : 256;
 };
 
 __host__ __device__ constexpr uint32_t prompt_idesc(int N, bool b_mn) {
@@ -198,10 +205,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const PromptAttnArgs a) {
   using Cfg = PromptCfg<D>;
-  constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages;
+  constexpr int NT = Cfg::kTiles, BN = Cfg::kKeys, ST = Cfg::kStages, PARTS = Cfg::kParts, THREADS = Cfg::kThreads;
+  constexpr bool OVER = Cfg::kOver;
   constexpr int MMA_WARP = Cfg::kSoftWarps, TMA_WARP = MMA_WARP + NT, PLAN_WARP = TMA_WARP + 1;
   extern __shared__ __align__(1024) uint8_t prompt_smem[];
-  __shared__ __align__(8) uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT][2], p_full[NT][2],
+  __shared__ __align__(8) uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], s_free[NT], p_full[NT][2],
       o_done[NT][2], v_raw, drain[NT], item_full[2], item_empty[2], answer_full;
   __shared__ __align__(16) uint8_t answer[16];
   __shared__ __align__(16) PromptItem items[2];
@@ -218,16 +226,17 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     abort_flag = 0;
     for (int s = 0; s < ST; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], NT);
+      mbar_init(&kv_empty[s], OVER ? 1 : NT);
     }
     for (int t = 0; t < NT; ++t) {
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&s_full[t][i], 1);
         mbar_init(&p_full[t][i], 4);  // the warps of a tile
         mbar_init(&o_done[t][i], 1);
       }
+      mbar_init(&s_full[t], 1);
+      mbar_init(&s_free[t], 4);
       mbar_init(&drain[t], 1);
     }
     mbar_init(&v_raw, 1);
@@ -287,211 +296,265 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     return true;
   };
 
-  if (warp == PLAN_WARP) {
-    // ---- a CTA number's tile pair: the borders are passed 32 sequences at a time, from where the last
-    // search ended (numbers mostly rise)
-    int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32
-    int cta = blockIdx.x;
-    uint32_t answers = 0;
-    bool more = true;
-    while (more) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[item_pos.s], item_pos.ph ^ 1u, &abort_flag));
-      if (!ok) break;
-      if (cta < 0) {  // not the first item
-        if (lane == 0) {
-          fence_proxy_async_shared();
-          mbar_arrive_expect_tx(&answer_full, 16);
-          cancel_next(answer, &answer_full);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&answer_full, answers & 1u, &abort_flag));
-        ++answers;
-        if (!ok) {
-          drain_wait(&answer_full, (answers - 1) & 1u);
-          break;
-        }
-        cta = cancelled_cta(answer);
-      }
-      PromptItem it = {-1, 0, 0, 0, 0, 0, {0, 0}};
-      if (cta == 0)
-        for (int b = lane; b < a.B; b += 32) {
-          int q, n, k, m;
-          if (!prompt_borders(a, b, q, n, k, m) || n > a.max_q) raise_error(kErrBadIndex);
-        }
-      if (cta >= 0) {
-        const int tile = cta / hx;
-        it.hq = cta % hx;
-        if (tile < base_tiles) base_b = base_tiles = 0;
-        while (base_b < a.B) {
-          const int b = base_b + lane;
-          int q, n = 0, k = 0, m = 0, tiles = 0;
-          if (b < a.B && prompt_borders(a, b, q, n, k, m))
-            tiles = ((n < a.max_q ? n : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
-          int upto = tiles;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+  // Two tiles: the softmax threads hold a row of 128 scores. The launch has 384 threads of 168 registers,
+  // 64512 in all; 256 x 208 + 128 x 88 are as many.
+  static_assert(NT == 1 || (THREADS == 384 && MMA_WARP == 8), "");
+  if (warp >= MMA_WARP) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == PLAN_WARP) {
+      // ---- a CTA number's tile pair: the borders are passed 32 sequences at a time, from where the last
+      // search ended (numbers mostly rise)
+      int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32
+      int cta = blockIdx.x;
+      uint32_t answers = 0;
+      bool more = true;
+      while (more) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[item_pos.s], item_pos.ph ^ 1u, &abort_flag));
+        if (!ok) break;
+        if (cta < 0) {  // not the first item
+          if (lane == 0) {
+            fence_proxy_async_shared();
+            mbar_arrive_expect_tx(&answer_full, 16);
+            cancel_next(answer, &answer_full);
           }
-          const int rank = tile - base_tiles;
-          const uint32_t here = __ballot_sync(0xffffffffu, rank < upto);
-          if (here != 0u) {  // the first sequence that reaches the rank; its last tokens see most keys
-            const int src = __ffs(here) - 1;
-            it.first = __shfl_sync(0xffffffffu, (upto - 1 - rank) * NT * per_tile, src);
-            it.q0 = __shfl_sync(0xffffffffu, q, src);
-            it.nq = __shfl_sync(0xffffffffu, n, src);
-            it.k0 = __shfl_sync(0xffffffffu, k, src);
-            it.nk = __shfl_sync(0xffffffffu, m, src);
+          ok = __all_sync(0xffffffffu, mbar_wait(&answer_full, answers & 1u, &abort_flag));
+          ++answers;
+          if (!ok) {
+            drain_wait(&answer_full, (answers - 1) & 1u);
             break;
           }
-          base_tiles += __shfl_sync(0xffffffffu, upto, 31);
-          base_b += 32;
+          cta = cancelled_cta(answer);
         }
-      }
-      more = it.first >= 0;
-      if (lane == 0) {
-        items[item_pos.s] = it;
-        mbar_arrive(&item_full[item_pos.s]);
-      }
-      item_pos.advance(1, 2);
-      cta = -1;
-    }
-  } else if (warp == TMA_WARP) {
-    RingPos pos;
-    int issued = 0;
-    uint32_t raws = 0, count[NT];  // copies on v_raw and q_full
+        PromptItem it = {-1, 0, 0, 0, 0, 0, {0, 0}};
+        if (cta == 0)
+          for (int b = lane; b < a.B; b += 32) {
+            int q, n, k, m;
+            if (!prompt_borders(a, b, q, n, k, m) || n > a.max_q) raise_error(kErrBadIndex);
+          }
+        if (cta >= 0) {
+          const int tile = cta / hx;
+          it.hq = cta % hx;
+          if (tile < base_tiles) base_b = base_tiles = 0;
+          while (base_b < a.B) {
+            const int b = base_b + lane;
+            int q, n = 0, k = 0, m = 0, tiles = 0;
+            if (b < a.B && prompt_borders(a, b, q, n, k, m))
+              tiles = ((n < a.max_q ? n : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
+            int upto = tiles;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) count[t] = 0;
-    while (next_item()) {
-      auto load = [&](const CUtensorMap* map, int j, uint64_t* full) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag));
-        if (!ok) return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, Cfg::kStageBytes);
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, full, 64 * c, hk, k0 + j * BN);
+            for (int o = 1; o < 32; o <<= 1) {
+              const int v = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += v;
+            }
+            const int rank = tile - base_tiles;
+            const uint32_t here = __ballot_sync(0xffffffffu, rank < upto);
+            if (here != 0u) {  // the first sequence that reaches the rank; its last tokens see most keys
+              const int src = __ffs(here) - 1;
+              it.first = __shfl_sync(0xffffffffu, (upto - 1 - rank) * NT * per_tile, src);
+              it.q0 = __shfl_sync(0xffffffffu, q, src);
+              it.nq = __shfl_sync(0xffffffffu, n, src);
+              it.k0 = __shfl_sync(0xffffffffu, k, src);
+              it.nk = __shfl_sync(0xffffffffu, m, src);
+              break;
+            }
+            base_tiles += __shfl_sync(0xffffffffu, upto, 31);
+            base_b += 32;
+          }
         }
-        if (full == &v_raw) {  // the last block, with rows that are no keys of the sequence
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raws & 1u, &abort_flag));
-          ++raws;
+        more = it.first >= 0;
+        if (lane == 0) {
+          items[item_pos.s] = it;
+          mbar_arrive(&item_full[item_pos.s]);
+        }
+        item_pos.advance(1, 2);
+        cta = -1;
+      }
+    } else if (warp == TMA_WARP) {
+      RingPos pos;
+      int issued = 0;
+      uint32_t raws = 0, count[NT];  // copies on v_raw and q_full
+#pragma unroll
+      for (int t = 0; t < NT; ++t) count[t] = 0;
+      while (next_item()) {
+        auto load = [&](const CUtensorMap* map, int j, uint64_t* full) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag));
           if (!ok) return;
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            for (int x = (nk - j * BN) * 8 + lane; x < BN * 8; x += 32)
-              reinterpret_cast<uint4*>(ring + pos.s * Cfg::kStageBytes + c * (BN * 128))[x] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[pos.s]);
-        }
-        pos.advance(1, ST);
-        ++issued;
-      };
-      auto load_q = [&](int t) {
-        if (blocks[t] == 0) return;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[t], (count[t] & 1u) ^ 1u, &abort_flag));
-        if (!ok) return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[t], Cfg::kQBytes);
-          for (int c = 0; c < Cfg::kChunks; ++c)
-            tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full[t], 64 * c, head0,
-                        q0 + first + t * per_tile);
-        }
-        ++count[t];
-      };
-      auto load_k = [&](int j) { load(&mapK, j, &kv_full[pos.s]); };
-      auto load_v = [&](int j) { load(&mapV, j, (j + 1) * BN > nk ? &v_raw : &kv_full[pos.s]); };
-      // in the order of the products below; the first K goes ahead, since its stage is free early
-      if (most > 0) load_k(0);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, Cfg::kStageBytes);
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, full, 64 * c, hk, k0 + j * BN);
+          }
+          if (full == &v_raw) {  // the last block, with rows that are no keys of the sequence
+            ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raws & 1u, &abort_flag));
+            ++raws;
+            if (!ok) return;
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              for (int x = (nk - j * BN) * 8 + lane; x < BN * 8; x += 32)
+                reinterpret_cast<uint4*>(ring + pos.s * Cfg::kStageBytes + c * (BN * 128))[x] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[pos.s]);
+          }
+          pos.advance(1, ST);
+          ++issued;
+        };
+        auto load_q = [&](int t) {
+          if (blocks[t] == 0) return;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[t], (count[t] & 1u) ^ 1u, &abort_flag));
+          if (!ok) return;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[t], Cfg::kQBytes);
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full[t], 64 * c, head0,
+                          q0 + first + t * per_tile);
+          }
+          ++count[t];
+        };
+        auto load_k = [&](int j) { load(&mapK, j, &kv_full[pos.s]); };
+        auto load_v = [&](int j) { load(&mapV, j, (j + 1) * BN > nk ? &v_raw : &kv_full[pos.s]); };
+        // in the order of the products below; the first K goes ahead, since its stage is free early
+        if (most > 0) load_k(0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) load_q(t);
-      for (int j = 0; j < most && ok; ++j) {
-        if (j + 1 < most) load_k(j + 1);
-        load_v(j);
+        for (int t = 0; t < NT; ++t) load_q(t);
+        for (int j = 0; j < most && ok; ++j) {
+          if (OVER) load_v(j);
+          if (j + 1 < most) load_k(j + 1);
+          if (!OVER) load_v(j);
+        }
+        if (!ok) break;
       }
-      if (!ok) break;
-    }
-    if (abort_flag) {  // no copy may still be landing when the CTA exits
-      for (int t = 0; t < NT; ++t)
-        if (count[t] > 0) drain_wait(&q_full[t], (count[t] - 1) & 1u);
-      drain_wait(&v_raw, raws & 1u);
-      for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
-    }
-  } else if (warp >= MMA_WARP) {
-    const int t = warp - MMA_WARP;
-    const uint32_t tm = (uint32_t)uniform((int)tmem);
-    constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
-    const uint64_t qd = smem_desc_sw128(smem_u32(smem + t * Cfg::kQBytes));
-    const uint64_t kd0 = smem_desc_sw128(smem_u32(ring));
-    const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(ring), BN * 128);
-    const uint32_t t_acc = tm + Cfg::kAcc + t * D, t_s = tm + 2 * t * Cfg::kScores;
-    RingPos pos;
-    uint32_t done = 0, queries = 0;  // key blocks of this tile so far, copies of its Q
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
-    };
-    auto scores = [&](uint32_t buf) {  // against the K block in the ring's current stage
-      const uint64_t kd = kd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
-      if (!elect_one()) return;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16_ss(t_s + buf * Cfg::kScores, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
-                    kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
-      mma_commit(&s_full[t][buf]);
-    };
-    auto weigh = [&](uint32_t buf, uint32_t acc) {  // with the V block in the ring's current stage
-      const uint64_t vd = vd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
-      if (!elect_one()) return;
-#pragma unroll
-      for (int k = 0; k < BN / 16; ++k)
-        mma_bf16_ts(t_acc, t_s + buf * Cfg::kScores + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o, k > 0 ? 1u : acc);
-      mma_commit(&o_done[t][buf]);
-    };
-    auto release = [&]() {  // the ring's current stage, once the products so far are done
-      if (ok && elect_one()) mma_commit(&kv_empty[pos.s]);
-      pos.advance(1, ST);
-    };
-    auto skip = [&]() {  // a block that only the other tile sees
-      wait(&kv_full[pos.s], pos.ph);
-      if (ok && lane == 0) mbar_arrive(&kv_empty[pos.s]);
-      pos.advance(1, ST);
-    };
-    while (next_item()) {
-      const int n = t == 0 ? blocks[0] : blocks[NT - 1], last = most;
-      // K 0, then K j + 1 and V j in turn: the next scores come before this block's weights are ready.
-      // The accumulator is free when the first weights are there, which come after the last output.
-      if (n > 0) {
-        wait(&q_full[t], queries & 1u);
-        ++queries;
-        wait(&kv_full[pos.s], pos.ph);
-        if (ok) scores(done & 1u);
-        release();
-        for (int j = 0; j < n - 1 && ok; ++j, ++done) {
-          wait(&kv_full[pos.s], pos.ph);
-          if (ok) scores((done + 1) & 1u);
-          if (j == n - 2 && ok && elect_one()) mma_commit(&q_empty[t]);
-          release();
-          wait(&kv_full[pos.s], pos.ph);
-          wait(&p_full[t][done & 1u], (done >> 1) & 1u);
-          tc_fence_after();
-          if (ok) weigh(done & 1u, j > 0);
-          release();
-        }
-        if (n == 1 && ok && elect_one()) mma_commit(&q_empty[t]);
-        if (n < last) skip();
-        wait(&kv_full[pos.s], pos.ph);
-        wait(&p_full[t][done & 1u], (done >> 1) & 1u);
+      if (abort_flag) {  // no copy may still be landing when the CTA exits
+        for (int t = 0; t < NT; ++t)
+          if (count[t] > 0) drain_wait(&q_full[t], (count[t] - 1) & 1u);
+        drain_wait(&v_raw, raws & 1u);
+        for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
+      }
+    } else {
+      // An issuing warp per tile; where the weights take the scores' place (OVER) the first one serves both,
+      // in turn: issued by two, the tiles' products would mix, all end late, and both softmaxes would run, then
+      // wait, together.
+      const int t = warp - MMA_WARP;
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
+      constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);
+      const uint64_t kd0 = smem_desc_sw128(smem_u32(ring));
+      const uint64_t vd0 = smem_desc_sw128_mn(smem_u32(ring), BN * 128);
+      RingPos pos;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag));
+      };
+      auto scores = [&](int u) {  // of tile u against the K block in the ring's current stage
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + u * Cfg::kQBytes));
+        const uint64_t kd = kd0 + (uint64_t)(pos.s * (Cfg::kStageBytes / 16));
         tc_fence_after();
-        if (ok) weigh(done & 1u, n > 1);
-        release();
-        ++done;
+        if (!ok || !elect_one()) return;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16_ss(tm + u * Cfg::kTileCols, qd + (uint64_t)(k / 4 * (128 * 128 / 16) + k % 4 * 2),
+                      kd + (uint64_t)(k / 4 * (BN * 128 / 16) + k % 4 * 2), id_s, k > 0);
+        mma_commit(&s_full[u]);
+      };
+      // block number x of tile u, its weights in buffer x & 1 of two, with the V block in ring stage vs
+      auto weigh = [&](int u, uint32_t x, int vs, uint32_t acc) {
+        const uint64_t vd = vd0 + (uint64_t)(vs * (Cfg::kStageBytes / 16));
+        const uint32_t t_p = tm + u * Cfg::kTileCols + Cfg::kWeights + (Cfg::kBuffers == 2 ? (x & 1u) * 32 : 0);
+        if (Cfg::kBuffers == 2) wait(&p_full[u][x & 1u], (x >> 1) & 1u);
+        else wait(&p_full[u][0], x & 1u);
+        tc_fence_after();
+        if (!ok || !elect_one()) return;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_bf16_ts(tm + Cfg::kAcc + u * D, t_p + k * 8, vd + (uint64_t)(k * (2048 / 16)), id_o, k > 0 ? 1u : acc);
+        mma_commit(&o_done[u][x & 1u]);
+      };
+      auto commit = [&](uint64_t* bar) {  // arrives once the products so far are done
+        if (ok && elect_one()) mma_commit(bar);
+      };
+      if constexpr (OVER) {
+        uint32_t done[2] = {0, 0}, queries[2] = {0, 0};  // key blocks of the tiles so far, copies of their Q
+        while (next_item()) {
+          if (t != 0 || most == 0) continue;
+          const int n[2] = {blocks[0], blocks[NT - 1]}, last = most;
+          // K 0, then V j and K j + 1 in turn
+          wait(&kv_full[pos.s], pos.ph);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (n[u] > 0) {
+              wait(&q_full[u], queries[u]++ & 1u);
+              scores(u);
+              if (n[u] == 1) commit(&q_empty[u]);
+            }
+          commit(&kv_empty[pos.s]);
+          pos.advance(1, ST);
+          for (int j = 0; j < last && ok; ++j) {
+            wait(&kv_full[pos.s], pos.ph);
+            const int vs = pos.s;
+            pos.advance(1, ST);
+            if (j + 1 < last) wait(&kv_full[pos.s], pos.ph);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (j < n[u]) weigh(u, done[u]++, vs, j > 0);
+              if (j + 1 < n[u]) {
+                scores(u);
+                if (j + 2 == n[u]) commit(&q_empty[u]);
+              }
+            }
+            commit(&kv_empty[vs]);
+            if (j + 1 < last) {
+              commit(&kv_empty[pos.s]);
+              pos.advance(1, ST);
+            }
+          }
+          if (!ok) break;
+        }
+      } else {
+        uint32_t done = 0, queries = 0;
+        auto skip = [&]() {  // a block that only the other tile sees
+          wait(&kv_full[pos.s], pos.ph);
+          if (ok && lane == 0) mbar_arrive(&kv_empty[pos.s]);
+          pos.advance(1, ST);
+        };
+        while (next_item()) {
+          const int n = t == 0 ? blocks[0] : blocks[NT - 1], last = most;
+          // K 0, then K j + 1 and V j in turn: the next scores come as soon as block j's have been read. The
+          // accumulator is free when the first weights are there, which come after the last output.
+          if (n > 0) {
+            wait(&q_full[t], queries++ & 1u);
+            wait(&kv_full[pos.s], pos.ph);
+            if (done > 0) wait(&s_free[t], (done - 1) & 1u);
+            scores(t);
+            if (n == 1) commit(&q_empty[t]);
+            commit(&kv_empty[pos.s]);
+            pos.advance(1, ST);
+            for (int j = 0; j < n && ok; ++j, ++done) {
+              if (j < n - 1) {
+                wait(&kv_full[pos.s], pos.ph);
+                wait(&s_free[t], done & 1u);
+                scores(t);
+                if (j == n - 2) commit(&q_empty[t]);
+                commit(&kv_empty[pos.s]);
+                pos.advance(1, ST);
+              } else if (n < last) {
+                skip();
+              }
+              wait(&kv_full[pos.s], pos.ph);
+              weigh(t, done, pos.s, j > 0);
+              commit(&kv_empty[pos.s]);
+              pos.advance(1, ST);
+            }
+          }
+          // what is left of the other tile's blocks
+          for (int x = n == 0 ? 0 : n == last ? 2 * n : 2 * n + 1; x < 2 * last && ok; ++x) skip();
+          if (!ok) break;
+        }
       }
-      for (int x = n > 0 ? 2 * n + (n < last ? 1 : 0) : 0; x < 2 * last && ok; ++x) skip();
-      if (!ok) break;
-    }
-    if (!ok && lane == 0) {  // no product may still be running when the CTA exits
-      mma_commit(&drain[t]);
-      drain_wait(&drain[t], 0);
+      if (!ok && lane == 0) {  // no product may still be running when the CTA exits
+        mma_commit(&drain[t]);
+        drain_wait(&drain[t], 0);
+      }
     }
   } else {
     // ---- softmax: a thread per row
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -506,19 +569,31 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       const int unmasked = seen(first + t * per_tile);  // keys that every row of the tile sees
       float m = -INFINITY, l = 0.f;
       float s[BN];
+      const uint32_t t_s = tmem + lanes + t * Cfg::kTileCols;
+      // Waits until block number x is in the accumulator. One barrier for even and one for odd blocks: when
+      // x is asked for, block x - 2 has been waited for (or this tile's next scores, which come later), and
+      // block x + 2 needs weights that this warp has not given yet, so that no phase is taken for another.
+      auto weighed = [&](uint32_t x) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t][x & 1u], (x >> 1) & 1u, &abort_flag));
+        tc_fence_after();
+        return ok;
+      };
       // the scores of the block number x, once they are there; asynchronous: tmem_ld_wait
       auto fetch = [&](uint32_t x) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t][x & 1u], (x >> 1) & 1u, &abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], x & 1u, &abort_flag));
         if (!ok) return;
         tc_fence_after();
-        const uint32_t t_s = tmem + lanes + (2 * t + (x & 1u)) * Cfg::kScores;
 #pragma unroll
         for (int c = 0; c < BN; c += 32) tmem_ld_nowait_x32(t_s + c, s + c);
       };
       if (n > 0) fetch(done);
       for (int j = 0; j < n && ok; ++j, ++done) {
-        const uint32_t t_s = tmem + lanes + (2 * t + (done & 1u)) * Cfg::kScores;
         tmem_ld_wait(s);
+        if (!OVER) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[t]);
+        }
         if (a.sign != 1.f) {
 #pragma unroll
           for (int c = 0; c < BN; ++c) s[c] *= a.sign;
@@ -543,13 +618,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
           const float f = up ? ex2_fast((m - mn) * sl2) : 1.f;
           m = mn;
           l *= f;
-          // the accumulator must hold the block before this one. (A barrier for even and one for odd blocks:
-          // these scores tell that the block before that is done, and the next one waits for these weights,
-          // so that neither an older nor a newer phase can be taken for it.)
-          ok = mbar_wait(&o_done[t][(done - 1) & 1u], ((done - 1) >> 1) & 1u, &abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
+          // the accumulator must hold the block before this one
+          if (!OVER) {
+            if (!weighed(done - 1)) break;
+          }
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -563,30 +635,35 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         const float shift = m == -INFINITY ? 0.f : -m * sl2;
         const F2 sl22(sl2, sl2), shift2(shift, shift);
         F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-        uint32_t p[BN / 2];
-#pragma unroll
-        for (int i = 0; i < BN / 2; ++i) {
-          float p0, p1;
-          fma2(F2(s[2 * i], s[2 * i + 1]), sl22, shift2).split(p0, p1);
-          p0 = ex2_fast(p0);
-          p1 = ex2_fast(p1);
-          sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
-          p[i] = pack_bf16(p0, p1);
+        if (!OVER && done >= Cfg::kBuffers) {  // the weights in this buffer have been used
+          if (!weighed(done - Cfg::kBuffers)) break;
         }
-        tmem_st_32x32b_x32(t_s, p);
-        if (j + 1 < n) fetch(done + 1);  // under the store
-        float l0, l1;
-        add2(sum[0], sum[1]).split(l0, l1);
-        l += l0 + l1;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float p0, p1;
+            fma2(F2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), sl22, shift2).split(p0, p1);
+            p0 = ex2_fast(p0);
+            p1 = ex2_fast(p1);
+            sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
+            p[i] = pack_bf16(p0, p1);
+          }
+          tmem_st_32x32b_x32(t_s + Cfg::kWeights + (Cfg::kBuffers == 2 ? (done & 1u) * 32 : h * 32), p);
+          if (!OVER && h == PARTS - 1 && j + 1 < n) fetch(done + 1);  // under the store
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t][done & 1u]);
+        if (lane == 0) mbar_arrive(&p_full[t][Cfg::kBuffers == 2 ? done & 1u : 0]);
+        float l0, l1;
+        add2(sum[0], sum[1]).split(l0, l1);
+        l += l0 + l1;
+        if (OVER && j + 1 < n) fetch(done + 1);
       }
       if (ok && n > 0) {
-        ok = mbar_wait(&o_done[t][(done - 1) & 1u], ((done - 1) >> 1) & 1u, &abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
+        weighed(done - 1);
       }
       const bool store = ok && token < nq;
       const float inv = l > 0.f ? 1.f / l : 0.f;
