@@ -329,58 +329,82 @@ def hbl_qkv_dequant(codes, gamma, D: int, bits: int, Y=None, stream=None):
     return Y
 
 
-def _rows(X, what: str):
-    """(pointer, elements between tokens) of bf16 states [T, H, D] whose token rows may lie apart
-    (a slice of a fused projection output); the heads of a token must be dense."""
+# The cache and attention calls are short enough on the GPU for their checks to count: one pass over
+# each tensor's shape, strides and device, and no lookups that torch repeats at every call.
+
+_torch = None
+
+
+def _load_torch():
+    global _torch, _bf16, _i32, _f32, _u8, _raw_stream, _current_device
     import torch
 
-    if X.dim() != 3 or X.dtype != torch.bfloat16:
+    _bf16, _i32, _f32, _u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
+
+
+def _device_of(t) -> int:
+    """The CUDA device that a call runs on: that of its first tensor."""
+    if _torch is None:
+        _load_torch()
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.get_device()
+
+
+def _rows(X, dev: int, what: str):
+    """(pointer, elements between tokens) of bf16 states [T, H, D] whose token rows may lie apart
+    (a slice of a fused projection output); the heads of a token must be dense."""
+    if X.dtype is not _bf16 or X.dim() != 3:
         raise ValueError(f"expected bf16 {what} [tokens, heads, D]")
     if not X.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    T, H, D = X.shape
-    st = X.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        raise ValueError(f"expected dense heads in {what}")
-    return X.data_ptr(), st[0] if T > 1 else H * D
-
-
-def _ints(t, n: int, like, what: str):
-    """Pointer of a contiguous int32 tensor of n entries on the device of `like`."""
-    import torch
-
-    if t.dtype != torch.int32 or t.numel() != n:
-        raise ValueError(f"expected int32 {what} of {n} entries")
-    _same_device(t, like)
-    return _ptr(t)
-
-
-def _same_device(t, like) -> None:
-    if t.device != like.device:
+    if X.get_device() != dev:
         raise ValueError("expected tensors on one device")
+    T, H, D = X.shape
+    s0, s1, s2 = X.stride()
+    if (D > 1 and s2 != 1) or (H > 1 and s1 != D):
+        raise ValueError(f"expected dense heads in {what}")
+    return X.data_ptr(), s0 if T > 1 else H * D
 
 
-def _out(t, shape, dtype, like, what: str):
-    """A given output of this shape and type, or a new one."""
-    import torch
+def _dense(t, dtype, dev: int, what: str) -> int:
+    """Pointer of a contiguous tensor of this type on this device."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"expected contiguous {dtype} {what}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError("expected tensors on one device")
+    return t.data_ptr()
 
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"expected {what} of shape {tuple(shape)} and type {dtype}")
-    _same_device(t, like)
-    return t
+
+def _ints(t, n: int, dev: int, what: str) -> int:
+    """Pointer of a contiguous int32 tensor of n entries."""
+    if t.numel() != n:
+        raise ValueError(f"expected int32 {what} of {n} entries")
+    return _dense(t, _i32, dev, what)
 
 
-def _call(f, name: str, like, args, stream) -> None:
+def _given(t, shape, dtype, dev: int, what: str) -> int:
+    """Pointer of an output that the caller gave."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"expected {what} of shape {shape}")
+    return _dense(t, dtype, dev, what)
+
+
+def _call(f, name: str, dev: int, args, stream) -> None:
     """The library call with the tensors' device current (its streams and launches belong to it)."""
-    import torch
-
-    if torch.cuda.current_device() != like.device.index:
-        with torch.cuda.device(like.device):
-            status = f(*args, _stream(stream, like))
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            status = f(*args, stream)
     else:
-        status = f(*args, _stream(stream, like))
+        status = f(*args, stream)
     if status != HBL_OK:
         raise HblError(status, name)
 
@@ -391,10 +415,6 @@ def hbl_kv_cache_bytes(num_pages: int, page_size: int, Hkv: int, D: int, bits: i
 
 def _num_pages(cache, page_size: int, Hkv: int, D: int, bits: int) -> int:
     """Whole pages that the cache buffer (uint8) holds."""
-    import torch
-
-    if cache.dtype != torch.uint8:
-        raise ValueError("expected a uint8 cache buffer")
     page = max(1, Hkv * (page_size // 16) * (4 * D * bits + 128))
     return min(cache.numel() // page, 0x7FFFFFFF // max(1, page_size))
 
@@ -404,41 +424,51 @@ def hbl_kv_append(K, V, slots, cache, page_size: int, bits: int = 3, pos=None, r
     """Write bf16 K, V [T, Hkv, D] into the paged cache (uint8 buffer of hbl_kv_cache_bytes) at `slots`
     (int32 [T]), quantised per head, K rotated when `pos` (int32 [T]) is given. With Q [T, Hq, D],
     returns Q rotated, bf16 (q_out may be Q itself); K, V and Q may be slices of a fused QKV output."""
-    import torch
-
+    dev = _device_of(K)
+    kp, ks = _rows(K, dev, "K")
+    vp, vs = _rows(V, dev, "V")
     T, Hkv, D = K.shape
     if V.shape != K.shape:
         raise ValueError("expected K and V of one shape")
-    kp, ks = _rows(K, "K")
-    vp, vs = _rows(V, "V")
-    _same_device(V, K)
-    _same_device(cache, K)
     Hq, qp, qs, op, os_ = 0, None, 0, None, 0
     if Q is not None:
+        qp, qs = _rows(Q, dev, "Q")
         if Q.shape[0] != T or Q.shape[2] != D:
             raise ValueError("expected Q with the tokens and the head size of K")
-        qp, qs = _rows(Q, "Q")
-        _same_device(Q, K)
         Hq = Q.shape[1]
-        q_out = _out(q_out, Q.shape, torch.bfloat16, K, "q_out")
-        op, os_ = _rows(q_out, "q_out")
-    _call(lib().hbl_kv_append, "hbl_kv_append", K,
-          (qp, qs, kp, ks, vp, vs, None if pos is None else _ints(pos, T, K, "pos"), _ints(slots, T, K, "slots"),
-           float(rope_theta), T, Hq, Hkv, D, bits, _ptr(cache), cache.numel(),
-           _num_pages(cache, page_size, Hkv, D, bits), page_size, op, os_), stream)
+        if q_out is None:
+            q_out = _torch.empty((T, Hq, D), dtype=_bf16, device=Q.device)
+            op, os_ = q_out.data_ptr(), Hq * D
+        else:
+            op, os_ = _rows(q_out, dev, "q_out")
+            if q_out.shape != Q.shape:
+                raise ValueError("expected q_out with the shape of Q")
+    cp = _dense(cache, _u8, dev, "cache")
+    _call((_lib or lib()).hbl_kv_append, "hbl_kv_append", dev,
+          (qp, qs, kp, ks, vp, vs, None if pos is None else _ints(pos, T, dev, "pos"), _ints(slots, T, dev, "slots"),
+           rope_theta, T, Hq, Hkv, D, bits, cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
+           op, os_), stream)
     return q_out
 
 
 def hbl_kv_gather(cache, slots, Hkv: int, D: int, page_size: int, bits: int = 3, K=None, V=None, stream=None):
     """The cached tokens at `slots` (int32 [T]) as bf16 (K, V) [T, Hkv, D]."""
-    import torch
-
+    dev = _device_of(cache)
+    cp = _dense(cache, _u8, dev, "cache")
     T = slots.numel()
-    K = _out(K, (T, Hkv, D), torch.bfloat16, cache, "K")
-    V = _out(V, (T, Hkv, D), torch.bfloat16, cache, "V")
-    _call(lib().hbl_kv_gather, "hbl_kv_gather", cache,
-          (_ptr(cache), cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
-           _ints(slots, T, cache, "slots"), T, Hkv, D, bits, _ptr(K), _ptr(V)), stream)
+    if K is None:
+        K = _torch.empty((T, Hkv, D), dtype=_bf16, device=cache.device)
+        kp = K.data_ptr()
+    else:
+        kp = _given(K, (T, Hkv, D), _bf16, dev, "K")
+    if V is None:
+        V = _torch.empty((T, Hkv, D), dtype=_bf16, device=cache.device)
+        vp = V.data_ptr()
+    else:
+        vp = _given(V, (T, Hkv, D), _bf16, dev, "V")
+    _call((_lib or lib()).hbl_kv_gather, "hbl_kv_gather", dev,
+          (cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size, _ints(slots, T, dev, "slots"), T,
+           Hkv, D, bits, kp, vp), stream)
     return K, V
 
 
@@ -451,24 +481,25 @@ def hbl_attn_decode(Q, cache, tables, lens, Hkv: int, page_size: int, bits: int 
     """Attention of bf16 Q [B, Hq, D] (one rotated token per sequence) over the paged cache: `tables`
     int32 [B, width] pages, `lens` int32 [B] tokens; scale defaults to 1/sqrt(D). Returns bf16
     O [B, Hq, D]; fills lse fp32 [B, Hq] when given."""
-    import torch
-
+    dev = _device_of(Q)
+    qp, qs = _rows(Q, dev, "Q")
     B, Hq, D = Q.shape
-    qp, qs = _rows(Q, "Q")
     if tables.dim() != 2 or tables.shape[0] != B:
         raise ValueError("expected tables [B, width]")
-    _same_device(cache, Q)
+    cp = _dense(cache, _u8, dev, "cache")
     if workspace is None:
         workspace = _u8_empty(hbl_attn_decode_workspace(B, Hq, Hkv, D), Q.device)
-    _same_device(workspace, Q)
-    O = _out(O, (B, Hq, D), torch.bfloat16, Q, "O")
-    if lse is not None:
-        _out(lse, (B, Hq), torch.float32, Q, "lse")
-    _call(lib().hbl_attn_decode, "hbl_attn_decode", Q,
-          (qp, qs, _ptr(cache), cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
-           _ints(tables, tables.numel(), Q, "tables"), tables.shape[1], _ints(lens, B, Q, "lens"), B, Hq, Hkv, D, bits,
-           float(D ** -0.5 if scale is None else scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-           _ptr(O), _ptr(lse)), stream)
+    wp = _dense(workspace, workspace.dtype, dev, "workspace")
+    if O is None:
+        O = _torch.empty((B, Hq, D), dtype=_bf16, device=Q.device)
+        op = O.data_ptr()
+    else:
+        op = _given(O, (B, Hq, D), _bf16, dev, "O")
+    _call((_lib or lib()).hbl_attn_decode, "hbl_attn_decode", dev,
+          (qp, qs, cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
+           _dense(tables, _i32, dev, "tables"), tables.shape[1], _ints(lens, B, dev, "lens"), B, Hq, Hkv, D, bits,
+           D ** -0.5 if scale is None else scale, wp, workspace.numel() * workspace.element_size(), op,
+           None if lse is None else _given(lse, (B, Hq), _f32, dev, "lse")), stream)
     return O
 
 
@@ -476,23 +507,22 @@ def hbl_attn_prompt(Q, K, V, cu_q, cu_k, max_q=None, scale=None, causal: bool = 
     """Attention over packed prompts: bf16 Q [total_q, Hq, D], K and V [total_k, Hkv, D], int32 cu_q and
     cu_k [B + 1] borders; max_q bounds the longest prompt's queries (default total_q); scale defaults
     to 1/sqrt(D). Returns bf16 O [total_q, Hq, D]; fills lse fp32 [total_q, Hq] when given."""
-    import torch
-
+    dev = _device_of(Q)
+    qp, qs = _rows(Q, dev, "Q")
+    kp, ks = _rows(K, dev, "K")
+    vp, vs = _rows(V, dev, "V")
     Tq, Hq, D = Q.shape
-    Tk, Hkv, _ = K.shape
-    if V.shape != K.shape or K.shape[2] != D:
+    Tk, Hkv, Dk = K.shape
+    if V.shape != K.shape or Dk != D:
         raise ValueError("expected K and V of one shape, with the head size of Q")
-    qp, qs = _rows(Q, "Q")
-    kp, ks = _rows(K, "K")
-    vp, vs = _rows(V, "V")
-    _same_device(K, Q)
-    _same_device(V, Q)
     B = cu_q.numel() - 1
-    O = _out(O, (Tq, Hq, D), torch.bfloat16, Q, "O")
-    if lse is not None:
-        _out(lse, (Tq, Hq), torch.float32, Q, "lse")
-    _call(lib().hbl_attn_prompt, "hbl_attn_prompt", Q,
-          (qp, qs, kp, ks, vp, vs, _ints(cu_q, B + 1, Q, "cu_q"), _ints(cu_k, B + 1, Q, "cu_k"), B, Tq, Tk,
-           Tq if max_q is None else int(max_q), Hq, Hkv, D, float(D ** -0.5 if scale is None else scale), int(causal),
-           _ptr(O), _ptr(lse)), stream)
+    if O is None:
+        O = _torch.empty((Tq, Hq, D), dtype=_bf16, device=Q.device)
+        op = O.data_ptr()
+    else:
+        op = _given(O, (Tq, Hq, D), _bf16, dev, "O")
+    _call((_lib or lib()).hbl_attn_prompt, "hbl_attn_prompt", dev,
+          (qp, qs, kp, ks, vp, vs, _ints(cu_q, B + 1, dev, "cu_q"), _ints(cu_k, B + 1, dev, "cu_k"), B, Tq, Tk,
+           Tq if max_q is None else int(max_q), Hq, Hkv, D, D ** -0.5 if scale is None else scale, int(causal), op,
+           None if lse is None else _given(lse, (Tq, Hq), _f32, dev, "lse")), stream)
     return O
