@@ -561,6 +561,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     const uint32_t t_acc = tmem + lanes + Cfg::kAcc + t * D;
     const float sl2 = a.scale_log2;
     const float slack = 8.f / sl2;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.O) & 31u) == 0;
     uint32_t done = 0;  // key blocks of this tile so far
     while (next_item()) {
       const int token = first + t * per_tile + row / a.pack, head = head0 + row % a.pack;
@@ -678,14 +679,17 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tmem_ld_wait(o);
           }
           if (store) {
-            uint4* dst = reinterpret_cast<uint4*>(a.O + ih * D + c);
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+            for (int e = 0; e < 16; ++e) w[e] = inv > 0.f ? pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+            uint16_t* dst = a.O + ih * D + c;
+            if (wide) {  // whole sectors
+              store_32(dst, w);
+              store_32(dst + 16, w + 8);
+            } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = inv > 0.f ? pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv) : 0u;
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
           }
         }
