@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
         for (int e = 0; e < 8; ++e) g = fmaxf(g, fabsf(w[e]));
 #pragma unroll
         for (int o = LPH / 2; o >= 1; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        const float mult = 0.5f * kL * rcp_approx(g);
+        const float mult = g > 0.f ? 0.5f * kL * rcp_approx(g) : 0.f;
         uint32_t y[8];  // the code plus the magic bits
         float d[8], far = 0.f;
         const F2 mult2(mult, mult), half2(0.5f * kL, 0.5f * kL), magic2(kMagic, kMagic), minus2(-1.f, -1.f);
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
 #pragma unroll
         for (int e = 0; e < 8; ++e) far = fmaxf(far, fabsf(d[e]));
         // in range, or the products may leave fp32's; written so that a NaN is not
-        const bool range = g > 1e-30f && g < 1e30f;
+        const bool range = g == 0.f || (g > 1e-30f && g < 1e30f);
         bool near = kind != 0 && !(range && far <= 0.5f - kNear);
         if (near) {
           // A zero is L/2 exactly, which the fp32 rounding takes to the even code: no border case,

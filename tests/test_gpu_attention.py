@@ -598,3 +598,161 @@ def test_a_block_from_qkv_to_wo(bits, Hq, Hkv, D):
     for i in range(steps):
         step([1] * len(lens), [n + i for n in lens])
     assert hbl.hbl_device_status() == hbl.HBL_OK
+
+
+# ------------------------------------------------------------------------- corners of the fast paths
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("rope", [True, False])
+def test_append_borders_and_zeros(bits, rope):
+    """Heads whose values lie on the codes' borders, just beside them, or are all zero: with a largest value
+    7 * 15 * 255 / 2^k-like, every multiple of gamma / L is a bf16 number."""
+    D, page, T, H = 128, 16, 64, 2
+    L = (1 << bits) - 1
+    rng = np.random.default_rng(bits)
+    x = np.zeros((T, 2 * H, D), np.float32)
+    for t in range(T):
+        for h in range(2 * H):
+            unit = 2.0 ** rng.integers(-3, 4)
+            if t % 4 == 0:      # borders: x = gamma m / L, gamma = L unit
+                x[t, h] = unit * rng.integers(-L, L + 1, D)
+            elif t % 4 == 1:    # one bf16 step beside them
+                x[t, h] = unit * rng.integers(-L, L + 1, D) * (1 + rng.choice([-1, 1], D) * 2.0 ** -8)
+            elif t % 4 == 2:    # next to the middle border
+                x[t, h] = unit * rng.choice([-1, 1], D) * 2.0 ** rng.integers(-40, 0, D)
+            if t % 4 != 3:
+                x[t, h, rng.integers(D)] = L * unit * (1 if t % 8 < 4 else -1)
+    b = inputs.f32_to_bf16_bits(x.reshape(T, -1)).reshape(T, 2 * H, D)
+    X = bf16(b)
+    pos = np.where(rng.random(T) < 0.5, 0, rng.integers(0, 5000, T)) if rope else None
+    cache = torch.zeros(hbl.hbl_kv_cache_bytes(T // page, page, H, D, bits), dtype=torch.uint8, device="cuda")
+    hbl.hbl_kv_append(X[:, :H], X[:, H:], i32(np.arange(T)), cache, page, bits, pos=None if pos is None else i32(pos))
+    uk, uv, gk, gv = split_records(cache.cpu().numpy(), H, D, bits, page)
+    for u, g, xs, p in ((uk, gk, b[:, :H], pos), (uv, gv, b[:, H:], None)):
+        ru, rg = quantise(xs, p, bits)
+        np.testing.assert_array_equal(u, ru)
+        np.testing.assert_allclose(g, rg, rtol=2.0 ** -21)
+
+
+def test_cache_past_4_gib():
+    # the same tokens in the last pages of a cache of more than 4 GiB and in a small one
+    Hkv, D, bits, page, n = 8, 128, 8, 64, 150
+    need = -(-n // page)
+    pages = (5 << 30) // hbl.hbl_kv_cache_bytes(1, page, Hkv, D, bits)
+    big = torch.empty(hbl.hbl_kv_cache_bytes(pages, page, Hkv, D, bits), dtype=torch.uint8, device="cuda")
+    small = torch.empty(hbl.hbl_kv_cache_bytes(need, page, Hkv, D, bits), dtype=torch.uint8, device="cuda")
+    assert big.numel() > 1 << 32
+    _, _, (Q, K, V) = fused_states(n, 16, Hkv, D, seed=2)
+    out = []
+    for cache, first in ((big, pages - need), (small, 0)):
+        slots = i32(first * page + np.arange(n))
+        hbl.hbl_kv_append(K, V, slots, cache, page, bits, pos=i32(np.arange(n)))
+        table = i32(first + np.arange(need)[None])
+        lse = torch.empty((1, 16), dtype=torch.float32, device="cuda")
+        o = hbl.hbl_attn_decode(Q[:1], cache, table, i32([n]), Hkv, page, bits, lse=lse)
+        out.append((*hbl.hbl_kv_gather(cache, slots, Hkv, D, page, bits), o, lse))
+    for a, b in zip(*out):
+        assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+    assert hbl.hbl_device_status() == hbl.HBL_OK
+
+
+def test_decode_wide_range_of_v_scales():
+    def mixed(low, high):
+        return lambda rng, g: np.where(rng.random(g.shape) < 0.3, high * g, low * g).astype(np.float32)
+
+    for low, high in ((1.0, 1e25), (1e-12, 1e12), (1e-35, 1e-30), (1e30, 1e36)):
+        c = decode_case([500, 77], 8, 2, 128, 3, 32, seed=12, gv=mixed(low, high))
+        check_decode(c, *run_decode(c))
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 9, 16, 17, 40])
+def test_decode_group_sizes(G):
+    for D, bits in ((64, 4), (128, 3), (256, 2)):
+        c = decode_case([333, 0, 64, 1], 2 * G, 2, D, bits, 64, seed=G)
+        check_decode(c, *run_decode(c))
+
+
+def test_outputs_at_16_byte_offsets():
+    c = prompt_case([200, 31], [200, 231], 4, 2, 128, seed=5)
+    ref, _ = run_prompt(c)
+    O = torch.empty(ref.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(ref.shape)
+    hbl.hbl_attn_prompt(c["Q"], c["K"], c["V"], i32(c["cq"]), i32(c["ck"]), O=O)
+    assert torch.equal(O, ref)
+    d = decode_case([70], 2, 1, 64, 4, 16, seed=5, dirty=False)
+    K, V = hbl.hbl_kv_gather(d["cache"], i32(np.arange(48)), 1, 64, 16, 4)
+    buf = torch.empty(2 * (K.numel() + 8), dtype=torch.bfloat16, device="cuda")
+    k, v = buf[8:8 + K.numel()].view(K.shape), buf[K.numel() + 16:].view(K.shape)
+    hbl.hbl_kv_gather(d["cache"], i32(np.arange(48)), 1, 64, 16, 4, K=k, V=v)
+    assert torch.equal(k, K) and torch.equal(v, V)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompt_rising_and_falling_scores(D):
+    # keys that grow from block to block move the running maximum again and again; shrinking ones never
+    for order in (1, -1):
+        c = prompt_case([140, 300], [1500, 300], 4, 2, D, seed=D)
+        for b in range(2):
+            n = int(c["ck"][b + 1] - c["ck"][b])
+            ramp = torch.linspace(0.1, 30.0, n, device="cuda")[::1 if order > 0 else 1]
+            ramp = ramp if order > 0 else ramp.flip(0)
+            c["K"][c["ck"][b]:c["ck"][b + 1]] *= ramp[:, None, None].to(torch.bfloat16)
+        check_prompt(c, *run_prompt(c))
+
+
+def test_prompt_many_sequences():
+    rng = np.random.default_rng(0)
+    nq = rng.integers(0, 9, 700)
+    nk = nq + rng.integers(0, 3, 700) * rng.integers(0, 40, 700)
+    nq[300], nk[300] = 700, 900
+    for causal in (True, False):
+        c = prompt_case(nq, nk, 2, 1, 64, seed=3, causal=causal)
+        check_prompt(c, *run_prompt(c))
+
+
+def test_calls_on_several_streams_at_once():
+    ps = [prompt_case([700 + i, 65], [900 + i, 65], 8, 2, 128, seed=30 + i) for i in range(3)]
+    ds = [decode_case([2000 + i, 5], 8, 2, 128, 3, 64, seed=40 + i, dirty=False) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        outs.clear()
+        for c, s in zip(ps + ds, streams):
+            with torch.cuda.stream(s):
+                outs.append(run_prompt(c) if "cq" in c else run_decode(c))
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(ps + ds, outs):
+        (check_prompt if "cq" in c else check_decode)(c, o, lse)
+
+
+def test_calls_on_a_given_stream():
+    c = decode_case([300], 4, 2, 128, 3, 64, seed=1, dirty=False)
+    ref = run_decode(c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(hbl.hbl_attn_decode_workspace(1, 4, 2, 128), dtype=torch.uint8, device="cuda")
+    O = torch.empty((1, 4, 128), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        O.zero_()
+        torch.cuda.synchronize()
+        run_decode(c, O=O, workspace=ws, stream=stream)
+        s.synchronize()
+        assert torch.equal(O, ref[0])
+
+
+def test_binding_refuses_mixed_tensors():
+    c = decode_case([40], 4, 2, 128, 3, 16, seed=1, dirty=False)
+    p = prompt_case([30], [30], 4, 2, 128, seed=1)
+    cq, ck = i32(p["cq"]), i32(p["ck"])
+    for f in (lambda: hbl.hbl_attn_decode(c["Q"], c["cache"].cpu(), c["t"], c["lens"], 2, 16, 3),
+              lambda: hbl.hbl_attn_decode(c["Q"], c["cache"], c["t"].long(), c["lens"], 2, 16, 3),
+              lambda: hbl.hbl_attn_decode(c["Q"], c["cache"], c["t"], c["lens"], 2, 16, 3, O=c["Q"].float()),
+              lambda: hbl.hbl_attn_prompt(p["Q"], p["K"], p["V"], cq.cpu(), ck),
+              lambda: hbl.hbl_attn_prompt(p["Q"], p["K"], p["V"], cq, ck[:1]),
+              lambda: hbl.hbl_attn_prompt(p["Q"].transpose(0, 1), p["K"], p["V"], cq, ck)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(hbl.HblError):  # a workspace that is too small
+        hbl.hbl_attn_decode(c["Q"], c["cache"], c["t"], c["lens"], 2, 16, 3,
+                            workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
