@@ -302,9 +302,20 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
   if (warp >= MMA_WARP) {
     if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == PLAN_WARP) {
-      // ---- a CTA number's tile pair: the borders are passed 32 sequences at a time, from where the last
-      // search ended (numbers mostly rise)
-      int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32
+      // ---- a CTA number's tile pair, from where the last search ended (numbers mostly rise). Up to 32
+      // sequences, causal: the pairs of most keys first, whatever their sequence (a level is a pair's place
+      // counted in pairs from its sequence's first key), so that the last ones are short. Else one sequence
+      // after the other, 32 at a time.
+      const bool by_level = a.causal && a.B <= 32;
+      int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32 (the current level)
+      int level = -1, top_level = -1, q_b = 0, n_b = 0, k_b = 0, m_b = 0, low_b = 0, tiles_b = 0;  // of lane b
+      if (by_level) {
+        if (lane < a.B && prompt_borders(a, lane, q_b, n_b, k_b, m_b))
+          tiles_b = ((n_b < a.max_q ? n_b : a.max_q) + NT * per_tile - 1) / (NT * per_tile);
+        low_b = m_b > n_b ? (m_b - n_b) / (NT * per_tile) : 0;
+        top_level = __reduce_max_sync(0xffffffffu, tiles_b > 0 ? low_b + tiles_b - 1 : -1);
+        level = top_level;
+      }
       int cta = blockIdx.x;
       uint32_t answers = 0;
       bool more = true;
@@ -334,8 +345,22 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         if (cta >= 0) {
           const int tile = cta / hx;
           it.hq = cta % hx;
-          if (tile < base_tiles) base_b = base_tiles = 0;
-          while (base_b < a.B) {
+          if (tile < base_tiles) base_b = base_tiles = 0, level = top_level;
+          for (; by_level && level >= 0; --level) {
+            const uint32_t there = __ballot_sync(0xffffffffu, level >= low_b && level < low_b + tiles_b);
+            const int rank = tile - base_tiles;
+            if (rank < __popc(there)) {
+              const int src = __fns(there, 0, rank + 1);
+              it.first = __shfl_sync(0xffffffffu, (level - low_b) * NT * per_tile, src);
+              it.q0 = __shfl_sync(0xffffffffu, q_b, src);
+              it.nq = __shfl_sync(0xffffffffu, n_b, src);
+              it.k0 = __shfl_sync(0xffffffffu, k_b, src);
+              it.nk = __shfl_sync(0xffffffffu, m_b, src);
+              break;
+            }
+            base_tiles += __popc(there);
+          }
+          while (!by_level && base_b < a.B) {
             const int b = base_b + lane;
             int q, n = 0, k = 0, m = 0, tiles = 0;
             if (b < a.B && prompt_borders(a, b, q, n, k, m))

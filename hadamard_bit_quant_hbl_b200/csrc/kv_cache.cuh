@@ -519,21 +519,31 @@ __global__ void __launch_bounds__(kGatherHeads * 2 * kGatherTokens * D / 32) kv_
   }
   const int per_page = a.c.page_size / kKvChunk, i = row % kKvChunk;
   const uint8_t* rec0 = a.c.base + ((size_t)page * a.c.Hkv * per_page + row / kKvChunk) * (size_t)Rec::kBytes;
-  for (int h = h0; h < a.c.Hkv; h += kGatherHeads * gridDim.y) {
+  // the next head's words are read before this one's values leave
+  uint32_t next[BITS];
+  float gamma = 0.f;
+  auto read = [&](int h) {
     const uint8_t* rec = rec0 + (size_t)h * per_page * Rec::kBytes;
-    uint32_t w[BITS], v[16];
-    const float step = reinterpret_cast<const float*>(rec + (which == 0 ? Rec::kGammaK : Rec::kGammaV))[i] / kL;
+    gamma = reinterpret_cast<const float*>(rec + (which == 0 ? Rec::kGammaK : Rec::kGammaV))[i];
     if (which == 0) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(rec + i * Rec::kRow) + g * BITS;
 #pragma unroll
-      for (int e = 0; e < BITS; ++e) w[e] = p[e];
-      kv_values<BITS, false>(w, step, v);
+      for (int e = 0; e < BITS; ++e) next[e] = p[e];
     } else {
       const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + Rec::kV) + 16 * (2 * g * BITS) + i;
 #pragma unroll
-      for (int e = 0; e < BITS; ++e) w[e] = (uint32_t)p[32 * e] | ((uint32_t)p[32 * e + 16] << 16);
-      kv_values<BITS, true>(w, step, v);
+      for (int e = 0; e < BITS; ++e) next[e] = (uint32_t)p[32 * e] | ((uint32_t)p[32 * e + 16] << 16);
     }
+  };
+  if (h0 < a.c.Hkv) read(h0);
+  for (int h = h0; h < a.c.Hkv; h += kGatherHeads * gridDim.y) {
+    uint32_t w[BITS], v[16];
+    const float step = gamma / kL;
+#pragma unroll
+    for (int e = 0; e < BITS; ++e) w[e] = next[e];
+    if (h + kGatherHeads * (int)gridDim.y < a.c.Hkv) read(h + kGatherHeads * gridDim.y);
+    if (which == 0) kv_values<BITS, false>(w, step, v);
+    else kv_values<BITS, true>(w, step, v);
     uint16_t* dst = out + ((size_t)t * a.c.Hkv + h) * D + 32 * g;
     if ((reinterpret_cast<uintptr_t>(out) & 31u) == 0) {
       store_32(dst, v);
