@@ -35,6 +35,10 @@
 // and never waits for another one: a piece of a sequence that it does not hold alone goes to the workspace
 // as (max, sum, o), and attn_decode_join_kernel adds the pieces in order. (Joining the four warps of a CTA
 // at each piece's end instead took 84 us against 64 for a ragged batch of 64 sequences up to 8192 tokens.)
+//
+// What bounds it is the integer pipe (a mask for every two codes) next to the copies: 64 sequences of 3500 to
+// 4096 tokens, 32 heads, three bits 194 us = 4.2 TB/s; one of 131072, 8 KV heads of 4 queries, four bits 40 us.
+// Three CTAs to an SM; a fourth, or deeper rings, gained nothing.
 #pragma once
 
 #include <cuda_fp16.h>

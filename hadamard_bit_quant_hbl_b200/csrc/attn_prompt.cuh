@@ -11,8 +11,8 @@
 // two divides their number, so that few tokens fill it too. A CTA holds two tiles of neighbouring tokens
 // (one for 256 features, whose accumulator takes half of tensor memory) and passes the key blocks once:
 //
-//   S = Q K^T      tcgen05.mma, both operands in shared memory, 64 keys in 64 columns of tensor memory
-//   P = exp2(scale log2(e) (S - m)), rounded to bf16, in two buffers of 32 columns; fp32 sums before rounding
+//   S = Q K^T      tcgen05.mma, both operands in shared memory, to tensor memory
+//   P = exp2(scale log2(e) (S - m)), rounded to bf16, in tensor memory; fp32 sums before rounding
 //   O += P V       tcgen05.mma, P from tensor memory, V as it lies (its features contiguous)
 //
 // The running maximum m moves only when a row's scores pass it by more than 8 binades of the weights
@@ -20,20 +20,24 @@
 // row, so its statistics need no exchange.
 //
 //   warps 0-3 (4-7)  softmax of the first (second) tile, then its output
-//   a warp per tile  one thread issues the tile's products: while one tile is in its softmax, the other's
-//                    P V and next S run. (One thread for both tiles was the limit: issuing a tile's 16
-//                    products took it 1300 to 1600 clocks next to the softmax warps, and each wait 200.)
-//   last warp        TMA copies of Q, then of K and V blocks through a ring. Rows of V behind a sequence's
+//   a warp per tile  an elected lane issues the tile's products from uniform operands (with divergent ones a
+//                    product took it 80 to 100 clocks, more than the tensor core). At 128 features the
+//                    first warp serves both tiles in turn, see PromptCfg::kOver
+//   next warp        TMA copies of Q, then of K and V blocks through a ring. Rows of V behind a sequence's
 //                    last key, which may hold anything, are cleared in shared memory (the scores of such
 //                    keys are replaced by -inf)
+//   last warp        plans: which tile pair comes next
 //
-//   a scheduling warp
+// One CTA per SM. The grid has a CTA per (tile pair, head group), the pairs of most keys first, but a running
+// CTA takes the places of those that have not started yet (cluster launch control), so that the copies of
+// the next pair's Q and its first scores run under the softmax and the output of this one. (A CTA for each
+// pair took 9 to 11 us of start and end.) Sizes of sequences are read on the device: the planning warp finds
+// a pair's sequence from the borders.
 //
-// One CTA per SM. The grid has a CTA per (tile pair, head group), the pairs of most keys of a sequence
-// first, but a running CTA takes the places of those that have not started yet (cluster launch control), so
-// that the copies of the next pair's Q and its first scores run under the softmax and the output of this one.
-// (A CTA for each pair took 9 to 11 us of start and end.) Sizes of sequences are read on the device: the
-// scheduling warp finds a pair's sequence from the borders.
+// Measured at 128 features: one 8192-token prompt of 32 heads 468 us (1175 TFLOP/s) in single calls, 558 us
+// (985 TFLOP/s) in a loop under the power cap; 12 packed prompts of 100 to 2400 tokens, 32 heads on 8, 197
+// and 227 us. What is left is the chain scores - softmax - weights - sums of a tile (about 3300 clocks a block
+// for 2048 clocks of products of both tiles).
 #pragma once
 
 #include <cuda.h>
@@ -75,8 +79,8 @@ __device__ __forceinline__ bool prompt_borders(const PromptAttnArgs& a, int b, i
 template <int D>
 struct PromptCfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;
-  // Keys of a block. A product of 128 rows reads its rows of Q in 64 clocks whatever its columns, so 128
-  // keys take no longer than 64; for 256 features shared memory has no room for them.
+  // Keys of a block. A product with 64 keys was measured at 62 clocks, as long as one with 128 (its rows of Q
+  // come from shared memory either way); for 256 features shared memory has no room for 128.
   static constexpr int kKeys = D == 256 ? 64 : 128;
   static constexpr int kParts = kKeys / 64;
   static constexpr int kChunks = D / 64;             // 128-byte columns of a row
@@ -456,8 +460,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       }
     } else {
       // An issuing warp per tile; where the weights take the scores' place (OVER) the first one serves both,
-      // in turn: issued by two, the tiles' products would mix, all end late, and both softmaxes would run, then
-      // wait, together.
+      // in turn: issued by two, the tiles' products mix, all end late, and both softmaxes run, then wait,
+      // together (one 8192-token prompt 510 us against 480; two warps that take turns 580).
       const int t = warp - MMA_WARP;
       const uint32_t tm = (uint32_t)uniform((int)tmem);
       constexpr uint32_t id_s = prompt_idesc(BN, false), id_o = prompt_idesc(D, true);

@@ -133,7 +133,7 @@ __device__ __forceinline__ void rope_cs(int pos, double inv_freq, float& c, floa
 
 // The codes (plus the bits of kAppendMagic) and gamma of a lane's eight values of a head, all in 64 bits.
 // Out of line: inlined, it and its sincos push the common path out of the instruction cache (8192 tokens of
-// 32 + 32 + 32 heads 398 us against @APPEND@).
+// 32 + 32 + 32 heads and their read-back 398 us against 236).
 constexpr float kAppendMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
 constexpr uint32_t kAppendMagicBits = 0x4b400000u;
 
@@ -178,7 +178,8 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
 // 2^-24, two roundings, of states up to sqrt(2) gamma), 0.75 from the reciprocal (one step) and its product,
 // 0.5 from the last sum. There the whole head is rotated, its gamma taken and its codes decided in fp64, so
 // that the codes are those of a 64-bit evaluation. A lane's eight values go two at a time through the
-// multiply-adds.
+// multiply-adds. Bound by latency and issue: 8192 tokens of 32 + 32 + 32 heads of 128 at three bits about
+// 105 us for 322 MB, 3.1 TB/s.
 template <int D, int BITS, bool ROPE>
 __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kernel(const KvAppendArgs a) {
   using Rec = KvRec<D, BITS>;
@@ -497,7 +498,8 @@ __device__ __forceinline__ void store_32(uint16_t* p, const uint32_t* v) {
 // x~ = (2u - L) gamma / L, rounded to bf16. One CTA takes 16 tokens and passes their heads two at a time; a
 // thread takes 32 features of K or of V of one token, the lanes consecutive tokens, so that V's interleaved
 // units are read as whole sectors and every thread writes two. Writing 4 D bytes for D b / 4 + 8 read, it is
-// bound by the stores: @GATHER@.
+// bound by the stores: 12.5 k tokens of 32
+// heads of 128 at three bits 57 us, 4.7 TB/s.
 template <int D, int BITS>
 __global__ void __launch_bounds__(kGatherHeads * 2 * kGatherTokens * D / 32) kv_gather_kernel(const KvGatherArgs a) {
   using Rec = KvRec<D, BITS>;
