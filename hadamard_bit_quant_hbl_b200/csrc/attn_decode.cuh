@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) attn_decode_join_kernel(const DecodeAttnArgs a) {
   constexpr int LANES = D / 4, GROUPS = THREADS / LANES;
-  __shared__ float f[kDecodeMaxUnits];
+  __shared__ float f[kDecodeMaxUnits], sums[kDecodeMaxUnits];
   __shared__ float red[THREADS / 32], parts[GROUPS][D];
   pdl_wait();
   pdl_launch_dependents();
@@ -804,9 +804,14 @@ __global__ void __launch_bounds__(THREADS) attn_decode_join_kernel(const DecodeA
   const size_t slot = (size_t)a.group * (D + 4);
   const float* w0 = a.ws + 2 * (size_t)ch.unit * slot;
   auto place = [&](int i) { return w0 + (2 * i + (i == 0 ? ch.first : 0)) * slot; };
+  // the first parts are on their way while the pieces' maxima are compared
+  const int d0 = threadIdx.x % LANES * 4, group = threadIdx.x / LANES;
+  auto part = [&](int i) { return *reinterpret_cast<const float4*>(place(i) + col * D + d0); };
+  float4 v = group < ch.n ? part(group) : make_float4(0.f, 0.f, 0.f, 0.f);
   float top = -INFINITY;
   for (int i = threadIdx.x; i < ch.n; i += THREADS) {
     f[i] = place(i)[a.group * D + col];
+    sums[i] = place(i)[a.group * D + a.group + col];
     top = fmaxf(top, f[i]);
   }
 #pragma unroll
@@ -819,7 +824,7 @@ __global__ void __launch_bounds__(THREADS) attn_decode_join_kernel(const DecodeA
   float sum = 0.f;
   for (int i = threadIdx.x; i < ch.n; i += THREADS) {
     f[i] = f[i] == -INFINITY ? 0.f : ex2_approx(f[i] - top);
-    sum = fmaf(f[i], place(i)[a.group * D + a.group + col], sum);
+    sum = fmaf(f[i], sums[i], sum);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -828,11 +833,10 @@ __global__ void __launch_bounds__(THREADS) attn_decode_join_kernel(const DecodeA
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) sum += red[w];
-  const int d0 = threadIdx.x % LANES * 4, group = threadIdx.x / LANES;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
   for (int i = group; i < ch.n; i += GROUPS) {
-    const float4 v = *reinterpret_cast<const float4*>(place(i) + col * D + d0);
+    if (i != group) v = part(i);
     o[0] = fmaf(f[i], v.x, o[0]);
     o[1] = fmaf(f[i], v.y, o[1]);
     o[2] = fmaf(f[i], v.z, o[2]);
