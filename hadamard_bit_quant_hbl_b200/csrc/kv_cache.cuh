@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
     uint2 lo[AHEAD], hi[AHEAD];
     auto load = [&](int t, uint2& l, uint2& u) {
       t = t < nt ? t : nt - 1;
-      l = *reinterpret_cast<const uint2*>(x + (size_t)t * stride);
-      u = *reinterpret_cast<const uint2*>(x + (size_t)t * stride + HALF);
+      l = __ldcs(reinterpret_cast<const uint2*>(x + (size_t)t * stride));  // read once
+      u = __ldcs(reinterpret_cast<const uint2*>(x + (size_t)t * stride + HALF));
     };
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) load(u, lo[u], hi[u]);
