@@ -90,6 +90,8 @@ struct PromptCfg {
   static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStageBytes;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kThreads = 32 * (kSoftWarps + kTiles + 2);
+  // Two tiles: registers of a thread at launch, and after the split between the softmax and the other warps
+  static constexpr int kRegisters = 168, kMoreRegisters = 208, kFewerRegisters = 88;
   // Tensor memory, 512 columns: each tile's scores and weights, then the accumulators. With 128 features
   // the weights take the scores' place, and the next scores wait until they have been used; elsewhere the
   // next scores come as soon as these have been read (two buffers of weights for blocks of 64 keys).
@@ -300,11 +302,11 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     return true;
   };
 
-  // Two tiles: the softmax threads hold a row of 128 scores. The launch has 384 threads of 168 registers,
-  // 64512 in all; 256 x 208 + 128 x 88 are as many.
-  static_assert(NT == 1 || (THREADS == 384 && MMA_WARP == 8), "");
+  // Two tiles: the softmax threads hold a row of 128 scores, so they take registers from the other warps.
+  static_assert(NT == 1 || (THREADS == 384 && MMA_WARP == 8 &&
+                            256 * Cfg::kMoreRegisters + 128 * Cfg::kFewerRegisters == 384 * Cfg::kRegisters), "");
   if (warp >= MMA_WARP) {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kFewerRegisters));
     if (warp == PLAN_WARP) {
       // ---- a CTA number's tile pair, from where the last search ended (numbers mostly rise). Up to 32
       // sequences, causal: the pairs of most keys first, whatever their sequence (a level is a pair's place
@@ -583,7 +585,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     }
   } else {
     // ---- softmax: a thread per row
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kMoreRegisters));
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

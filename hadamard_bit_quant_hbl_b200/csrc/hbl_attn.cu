@@ -117,6 +117,14 @@ hbl_status launch_prompt(const PromptAttnArgs& a, cudaStream_t s) {
   auto* k = attn_prompt_kernel<D>;
   const cudaError_t e = allow_smem(k, Cfg::kSmem, lim);
   if (e != cudaSuccess) return cuda_fail(e);
+  if (Cfg::kTiles == 2) {
+    // the kernel hands registers from some warps to others, which needs the launch to bring them all
+    static const int regs = [k] {
+      cudaFuncAttributes at;
+      return cudaFuncGetAttributes(&at, k) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != Cfg::kRegisters) return HBL_EUNSUPPORTED;
+  }
   CUtensorMap mq, mk, mv;
   if (!make_map_rows(&mq, a.Q, a.q_stride, a.total_q, a.Hq, D, a.pack, 128 / a.pack)) return HBL_ECUDA;
   if (a.total_k > 0) {

@@ -144,3 +144,26 @@ def test_library_call_with_null_stream_argument_types(L):
     # the C signatures as declared: sizes are 64-bit, a call with a size past 32 bits is checked as such
     assert L.hbl_kv_gather.argtypes[1] is ctypes.c_size_t
     assert L.hbl_attn_decode.argtypes[16] is ctypes.c_size_t
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_a_masked_half_word_is_an_fp16_operand(bits):
+    # u << p inside a half-word is the fp16 number u 2^(p - 24) as long as it stays below 2^11
+    u = np.arange(1 << bits, dtype=np.uint16)
+    p = 0
+    while ((1 << bits) - 1) << p < 1 << 11:
+        np.testing.assert_array_equal((u << p).astype(np.uint16).view(np.float16).astype(np.float64), u * 2.0 ** (p - 24))
+        p += 1
+    assert p > {2: 8, 3: 6, 4: 4, 8: 0}[bits]  # the highest place that the decode uses
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_a_code_becomes_its_state_by_one_exact_multiply_add(bits):
+    # the code at bit p >= 1 with the bits of 2^23 above it is 2^23 + u 2^p; times 2 / 2^p, less 2^24 / 2^p + L
+    L = (1 << bits) - 1
+    u = np.arange(L + 1, dtype=np.uint32)
+    for p in range(1, 17 - bits + 1):
+        f = ((u << p) | np.uint32(0x4B000000)).view(np.float32).astype(np.float64)
+        a, b = 2.0 / 2 ** p, 2.0 ** 24 / 2 ** p + L
+        assert float(np.float32(a)) == a and float(np.float32(b)) == b
+        np.testing.assert_array_equal(f * a - b, 2.0 * u - L)
