@@ -37,7 +37,7 @@
 // at each piece's end instead took 84 us against 64 for a ragged batch of 64 sequences up to 8192 tokens.)
 //
 // What bounds it is the integer pipe (a mask for every two codes) next to the copies: 64 sequences of 3500 to
-// 4096 tokens, 32 heads, three bits 194 us = 4.2 TB/s; one of 131072, 8 KV heads of 4 queries, four bits 40 us.
+// 4096 tokens, 32 heads, three bits 192 us = 4.2 TB/s; one of 131072, 8 KV heads of 4 queries, four bits 39 us.
 // Three CTAs to an SM; a fourth, or deeper rings, gained nothing.
 #pragma once
 

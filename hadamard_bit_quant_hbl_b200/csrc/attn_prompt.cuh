@@ -34,9 +34,9 @@
 // pair took 9 to 11 us of start and end.) Sizes of sequences are read on the device: the planning warp finds
 // a pair's sequence from the borders.
 //
-// Measured at 128 features: one 8192-token prompt of 32 heads 468 us (1175 TFLOP/s) in single calls, 558 us
-// (985 TFLOP/s) in a loop under the power cap; 12 packed prompts of 100 to 2400 tokens, 32 heads on 8, 197
-// and 227 us. What is left is the chain scores - softmax - weights - sums of a tile (about 3300 clocks a block
+// Measured at 128 features: one 8192-token prompt of 32 heads 468 us (1175 TFLOP/s) in single calls, 553 us
+// (994 TFLOP/s) in a loop under the power cap; 12 packed prompts of 100 to 2400 tokens, 32 heads on 8, 197
+// and 225 us. What is left is the chain scores - softmax - weights - sums of a tile (about 3300 clocks a block
 // for 2048 clocks of products of both tiles).
 #pragma once
 
