@@ -394,17 +394,22 @@ def _given(t, shape, dtype, dev: int, what: str) -> int:
     return _dense(t, dtype, dev, what)
 
 
-def _call(f, name: str, dev: int, args, stream) -> None:
-    """The library call with the tensors' device current (its streams and launches belong to it)."""
-    if stream is None:
-        stream = _raw_stream(dev)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+def _on(stream, dev: int):
+    """The given stream (a torch stream or its handle) as the current one, so that what the call allocates
+    belongs to it: memory of another stream could be in use there, or be used again too early."""
+    if isinstance(stream, int):
+        stream = _torch.cuda.ExternalStream(stream, device=dev)
+    return _torch.cuda.stream(stream)
+
+
+def _call(f, name: str, dev: int, args) -> None:
+    """The library call on the current stream, with the tensors' device current (its streams and launches
+    belong to it)."""
     if _current_device() != dev:
         with _torch.cuda.device(dev):
-            status = f(*args, stream)
+            status = f(*args, _raw_stream(dev))
     else:
-        status = f(*args, stream)
+        status = f(*args, _raw_stream(dev))
     if status != HBL_OK:
         raise HblError(status, name)
 
@@ -425,6 +430,9 @@ def hbl_kv_append(K, V, slots, cache, page_size: int, bits: int = 3, pos=None, r
     (int32 [T]), quantised per head, K rotated when `pos` (int32 [T]) is given. With Q [T, Hq, D],
     returns Q rotated, bf16 (q_out may be Q itself); K, V and Q may be slices of a fused QKV output."""
     dev = _device_of(K)
+    if stream is not None:
+        with _on(stream, dev):
+            return hbl_kv_append(K, V, slots, cache, page_size, bits, pos, rope_theta, Q, q_out)
     kp, ks = _rows(K, dev, "K")
     vp, vs = _rows(V, dev, "V")
     T, Hkv, D = K.shape
@@ -447,13 +455,16 @@ def hbl_kv_append(K, V, slots, cache, page_size: int, bits: int = 3, pos=None, r
     _call((_lib or lib()).hbl_kv_append, "hbl_kv_append", dev,
           (qp, qs, kp, ks, vp, vs, None if pos is None else _ints(pos, T, dev, "pos"), _ints(slots, T, dev, "slots"),
            rope_theta, T, Hq, Hkv, D, bits, cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
-           op, os_), stream)
+           op, os_))
     return q_out
 
 
 def hbl_kv_gather(cache, slots, Hkv: int, D: int, page_size: int, bits: int = 3, K=None, V=None, stream=None):
     """The cached tokens at `slots` (int32 [T]) as bf16 (K, V) [T, Hkv, D]."""
     dev = _device_of(cache)
+    if stream is not None:
+        with _on(stream, dev):
+            return hbl_kv_gather(cache, slots, Hkv, D, page_size, bits, K, V)
     cp = _dense(cache, _u8, dev, "cache")
     T = slots.numel()
     if K is None:
@@ -468,7 +479,7 @@ def hbl_kv_gather(cache, slots, Hkv: int, D: int, page_size: int, bits: int = 3,
         vp = _given(V, (T, Hkv, D), _bf16, dev, "V")
     _call((_lib or lib()).hbl_kv_gather, "hbl_kv_gather", dev,
           (cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size, _ints(slots, T, dev, "slots"), T,
-           Hkv, D, bits, kp, vp), stream)
+           Hkv, D, bits, kp, vp))
     return K, V
 
 
@@ -482,6 +493,9 @@ def hbl_attn_decode(Q, cache, tables, lens, Hkv: int, page_size: int, bits: int 
     int32 [B, width] pages, `lens` int32 [B] tokens; scale defaults to 1/sqrt(D). Returns bf16
     O [B, Hq, D]; fills lse fp32 [B, Hq] when given."""
     dev = _device_of(Q)
+    if stream is not None:
+        with _on(stream, dev):
+            return hbl_attn_decode(Q, cache, tables, lens, Hkv, page_size, bits, scale, workspace, O, lse)
     qp, qs = _rows(Q, dev, "Q")
     B, Hq, D = Q.shape
     if tables.dim() != 2 or tables.shape[0] != B:
@@ -499,7 +513,7 @@ def hbl_attn_decode(Q, cache, tables, lens, Hkv: int, page_size: int, bits: int 
           (qp, qs, cp, cache.numel(), _num_pages(cache, page_size, Hkv, D, bits), page_size,
            _dense(tables, _i32, dev, "tables"), tables.shape[1], _ints(lens, B, dev, "lens"), B, Hq, Hkv, D, bits,
            D ** -0.5 if scale is None else scale, wp, workspace.numel() * workspace.element_size(), op,
-           None if lse is None else _given(lse, (B, Hq), _f32, dev, "lse")), stream)
+           None if lse is None else _given(lse, (B, Hq), _f32, dev, "lse")))
     return O
 
 
@@ -508,6 +522,9 @@ def hbl_attn_prompt(Q, K, V, cu_q, cu_k, max_q=None, scale=None, causal: bool = 
     cu_k [B + 1] borders; max_q bounds the longest prompt's queries (default total_q); scale defaults
     to 1/sqrt(D). Returns bf16 O [total_q, Hq, D]; fills lse fp32 [total_q, Hq] when given."""
     dev = _device_of(Q)
+    if stream is not None:
+        with _on(stream, dev):
+            return hbl_attn_prompt(Q, K, V, cu_q, cu_k, max_q, scale, causal, O, lse)
     qp, qs = _rows(Q, dev, "Q")
     kp, ks = _rows(K, dev, "K")
     vp, vs = _rows(V, dev, "V")
@@ -524,5 +541,5 @@ def hbl_attn_prompt(Q, K, V, cu_q, cu_k, max_q=None, scale=None, causal: bool = 
     _call((_lib or lib()).hbl_attn_prompt, "hbl_attn_prompt", dev,
           (qp, qs, kp, ks, vp, vs, _ints(cu_q, B + 1, dev, "cu_q"), _ints(cu_k, B + 1, dev, "cu_k"), B, Tq, Tk,
            Tq if max_q is None else int(max_q), Hq, Hkv, D, D ** -0.5 if scale is None else scale, int(causal), op,
-           None if lse is None else _given(lse, (Tq, Hq), _f32, dev, "lse")), stream)
+           None if lse is None else _given(lse, (Tq, Hq), _f32, dev, "lse")))
     return O

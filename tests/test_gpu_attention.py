@@ -756,3 +756,25 @@ def test_binding_refuses_mixed_tensors():
     with pytest.raises(hbl.HblError):  # a workspace that is too small
         hbl.hbl_attn_decode(c["Q"], c["cache"], c["t"], c["lens"], 2, 16, 3,
                             workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def test_given_stream_owns_what_a_call_allocates():
+    """Outputs and workspaces of calls on a given stream belong to it: work and allocations that follow at
+    once on the current stream leave them alone."""
+    c = decode_case([3000, 500], 8, 2, 128, 3, 64, seed=2, dirty=False)
+    p = prompt_case([1500], [1500], 8, 2, 128, seed=2)
+    ref_d, ref_p = run_decode(c)[0], run_prompt(p)[0]
+    slots = i32(np.arange(64))
+    ref_k, _ = hbl.hbl_kv_gather(c["cache"], slots, 2, 128, 64, 3)
+    s = torch.cuda.Stream()
+    cq, ck = i32(p["cq"]), i32(p["ck"])
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        for _ in range(5):
+            o = hbl.hbl_attn_decode(c["Q"], c["cache"], c["t"], c["lens"], 2, 64, 3, scale=c["scale"], stream=stream)
+            q = hbl.hbl_attn_prompt(p["Q"], p["K"], p["V"], cq, ck, stream=stream)
+            k, _ = hbl.hbl_kv_gather(c["cache"], slots, 2, 128, 64, 3, stream=stream)
+            for n in (hbl.hbl_attn_decode_workspace(2, 8, 2, 128), o.numel() * 2, q.numel() * 2):
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+            torch.cuda.synchronize()
+            assert torch.equal(o, ref_d) and torch.equal(q, ref_p) and torch.equal(k, ref_k)
