@@ -44,6 +44,8 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "drain.cuh"
+#include "gemm_swap.cuh"
 #include "kv_cache.cuh"
 
 namespace hbl {
@@ -417,6 +419,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
   Piece ahead = piece;
   int aj = ahead.j0;  // the next block of `ahead`
   bool more = true;
+  RingCopies<ST> copies;
   const int per_page = a.c.page_size / kKvChunk;
   const bool whole_blocks = per_page % CH == 0;  // a block's records lie side by side
   int pages[CH];
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
           if (good[i]) bulk_load_1d(dst + i * Rec::kBytes, source(pages[i], c0 + i), Rec::kBytes, bar);
       }
     }
+    copies.start();
     ++aj;
     settle();
   };
@@ -484,8 +488,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
   // fragment row r of a 16-token chunk is token 4(r/2) + r%2 for r < 8, two more for r >= 8, so that the
   // transposed weights' pairs of tokens are those of the words v_codes loads
   const int row0 = 4 * (g >> 1) + (g & 1);
-  RingPos pos;
-  bool first_piece = true;
+  bool first_piece = true, ok = true;
   while (true) {
     // ---- q of this piece: fragment of the head in column g of each tile
     const int hk = piece.h / a.groups, hg = piece.h % a.groups;
@@ -568,8 +571,10 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
     }
 
     for (int at = piece.j0; at < piece.j1; ++at) {
-      if (!mbar_wait(&bars[warp][pos.s], pos.ph, &abort_flag)) more = false;  // flagged: copy nothing more
-      const uint8_t* stage = ring + pos.s * Cfg::kStageBytes;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][copies.stage], copies.parity, &abort_flag));
+      if (!ok) break;  // flagged
+      const int st = copies.stage;
+      const uint8_t* stage = ring + st * Cfg::kStageBytes;
 #pragma unroll
       for (int c0 = 0; c0 < CH; c0 += R * SUB) {
         float z[SUB][NT][4];  // score + binade of gammaV
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
           }
           const int mine = c0 + u * R + 2 * j / GW;  // the chunk of this lane's columns
           const uint8_t* rec = stage + mine * Rec::kBytes;
-          const int nv = valid[warp][pos.s][mine];
+          const int nv = valid[warp][st][mine];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int row = row0 + 2 * r;
@@ -694,9 +699,10 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
         }
       }
       __syncwarp();  // every lane is done with the stage
-      copy(pos.s);
-      pos.advance(1, ST);
+      copies.use();
+      copy(st);
     }
+    if (!ok) break;
 
     // ---- join the column groups, then the output or the piece's part of it
     const int nb = (piece.len + Cfg::kBlock - 1) / Cfg::kBlock;
@@ -781,6 +787,12 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
     }
     if (!piece.next(a)) break;
     first_piece = false;
+  }
+  if (!ok) {  // no copy may still be landing when the CTA exits, and the join has nothing of these pieces to add
+    copies.drain([&](int s, uint32_t parity) { drain_wait(&bars[warp][s], parity); });
+    do {
+      if (piece.j0 == 0 && lane == 0) a.chains[(size_t)piece.b * hcols + piece.h] = DecodeChain{unit, 1, 0, 0};
+    } while (piece.next(a));
   }
 }
 
