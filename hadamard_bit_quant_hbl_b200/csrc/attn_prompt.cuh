@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "drain.cuh"
 #include "gemm_swap.cuh"
 #include "gemm_tc.cuh"
 #include "kv_cache.cuh"
@@ -403,9 +404,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     } else if (warp == TMA_WARP) {
       RingPos pos;
       int issued = 0;
-      uint32_t raws = 0, count[NT];  // copies on v_raw and q_full
-#pragma unroll
-      for (int t = 0; t < NT; ++t) count[t] = 0;
+      LoneCopies raws, queries[NT];  // on v_raw and q_full
       while (next_item()) {
         auto load = [&](const CUtensorMap* map, int j, uint64_t* full) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[pos.s], pos.ph ^ 1u, &abort_flag));
@@ -416,8 +415,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
               tma_load_3d(ring + pos.s * Cfg::kStageBytes + c * (BN * 128), map, full, 64 * c, hk, k0 + j * BN);
           }
           if (full == &v_raw) {  // the last block, with rows that are no keys of the sequence
-            ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raws & 1u, &abort_flag));
-            ++raws;
+            raws.start();
+            ok = __all_sync(0xffffffffu, mbar_wait(&v_raw, raws.parity(), &abort_flag));
             if (!ok) return;
             for (int c = 0; c < Cfg::kChunks; ++c)
               for (int x = (nk - j * BN) * 8 + lane; x < BN * 8; x += 32)
@@ -431,7 +430,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         };
         auto load_q = [&](int t) {
           if (blocks[t] == 0) return;
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[t], (count[t] & 1u) ^ 1u, &abort_flag));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[t], (queries[t].started & 1u) ^ 1u, &abort_flag));
           if (!ok) return;
           if (lane == 0) {
             mbar_arrive_expect_tx(&q_full[t], Cfg::kQBytes);
@@ -439,7 +438,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
               tma_load_3d(smem + t * Cfg::kQBytes + c * (128 * 128), &mapQ, &q_full[t], 64 * c, head0,
                           q0 + first + t * per_tile);
           }
-          ++count[t];
+          queries[t].start();
         };
         auto load_k = [&](int j) { load(&mapK, j, &kv_full[pos.s]); };
         auto load_v = [&](int j) { load(&mapV, j, (j + 1) * BN > nk ? &v_raw : &kv_full[pos.s]); };
@@ -455,9 +454,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         if (!ok) break;
       }
       if (abort_flag) {  // no copy may still be landing when the CTA exits
-        for (int t = 0; t < NT; ++t)
-          if (count[t] > 0) drain_wait(&q_full[t], (count[t] - 1) & 1u);
-        drain_wait(&v_raw, raws & 1u);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) queries[t].drain([&](uint32_t parity) { drain_wait(&q_full[t], parity); });
+        raws.drain([&](uint32_t parity) { drain_wait(&v_raw, parity); });
         for (int d = issued > ST ? issued - ST : 0; d < issued; ++d) drain_wait(&kv_full[d % ST], (uint32_t)(d / ST) & 1u);
       }
     } else {

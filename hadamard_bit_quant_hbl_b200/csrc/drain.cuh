@@ -12,6 +12,19 @@
 
 namespace hbl {
 
+// Copies counted on one barrier, each started after the one before it has been waited for: number i (from 0)
+// completes phase i, whose parity is i & 1.
+struct LoneCopies {
+  uint32_t started = 0;
+  HBL_COUNT void start() { ++started; }
+  HBL_COUNT uint32_t parity() const { return (started - 1u) & 1u; }  // of the newest one's phase
+  // wait(parity) for the newest one, which may still be landing
+  template <typename W>
+  HBL_COUNT void drain(W wait) const {
+    if (started > 0) wait(parity());
+  }
+};
+
 // Copies through a ring of N barriers, started and used in the same order, at most N started ahead of the
 // oldest one that has not been used.
 template <int N>

@@ -27,6 +27,26 @@ static void drain_wait(Barrier& b, unsigned parity) {
   }
 }
 
+// One barrier, a copy at a time.
+static void lone(unsigned seed) {
+  std::srand(seed);
+  Barrier b;
+  hbl::LoneCopies c;
+  for (int left = std::rand() % 5; left > 0; --left) {
+    ++b.started;
+    c.start();
+    bool gave_up = false;
+    while (!b.done(c.parity()) && !gave_up) {
+      if (std::rand() % 2) ++b.landed;
+      else gave_up = std::rand() % 4 == 0;
+    }
+    if (gave_up) break;
+    expect(b.landed == b.started, "a wait is over before its copy has landed");
+  }
+  c.drain([&](unsigned parity) { drain_wait(b, parity); });
+  expect(b.landed == b.started, "a copy is in flight after the drain");
+}
+
 template <int N>
 static void ring(unsigned seed) {
   std::srand(seed);
@@ -67,6 +87,7 @@ static void ring(unsigned seed) {
 
 int main() {
   for (unsigned seed = 0; seed < 20000; ++seed) {
+    lone(seed);
     ring<1>(seed);
     ring<2>(seed);
     ring<3>(seed);
