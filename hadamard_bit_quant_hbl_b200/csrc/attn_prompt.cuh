@@ -577,7 +577,8 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
           if (!ok) break;
         }
       }
-      if (!ok && lane == 0) {  // no product may still be running when the CTA exits
+      // no product may still be running when the CTA exits; a commit counts those of the thread that gives it
+      if (!ok && elect_one()) {
         mma_commit(&drain[t]);
         drain_wait(&drain[t], 0);
       }
