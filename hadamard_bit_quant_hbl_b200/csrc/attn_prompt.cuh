@@ -698,9 +698,10 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         weighed(done - 1);
       }
       const bool store = ok && token < nq;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool some = l != 0.f;  // sees a key; a NaN among its scores is one in l, and stays one
+      const float inv = some ? 1.f / l : 0.f;
       const size_t ih = (size_t)(q0 + token) * a.Hq + head;
-      if (store && a.lse) a.lse[ih] = l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      if (store && a.lse) a.lse[ih] = some ? (m * sl2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
       if (ok) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -712,7 +713,7 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
           if (store) {
             uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = inv > 0.f ? pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+            for (int e = 0; e < 16; ++e) w[e] = some ? pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
             uint16_t* dst = a.O + ih * D + c;
             if (wide) {  // whole sectors
               store_32(dst, w);

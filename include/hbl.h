@@ -343,7 +343,8 @@ hbl_status hbl_attn_decode(const void* Q, size_t q_stride, const void* cache, si
 /* Attention over packed prompts: sequence b has queries cu_q[b] .. cu_q[b+1]-1 and keys
  * cu_k[b] .. cu_k[b+1]-1 (a cached prefix first, when there are more keys than queries).
  *   causal  query i of nq sees keys j <= i + nk - nq of nk; 0: all keys of its sequence. A query that
- *           sees no key gives o = 0 and lse = -inf
+ *           sees no key gives o = 0 and lse = -inf. A NaN among the scores that a query sees
+ *           (from Q or K, or an infinity less an infinity) makes that query and head NaN, lse included
  *   Q, K, V device bf16 rows as in hbl_kv_append (K rotated)
  *   cu_q, cu_k  device int32 [B + 1], not decreasing, 0 <= cu_q <= total_q, 0 <= cu_k <= total_k.
  *           A sequence whose borders are not so is left out and flagged (hbl_device_status). Rows
