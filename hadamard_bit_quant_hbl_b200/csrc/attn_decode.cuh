@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
             const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[row];
             const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[row];
             int e = (int)((__float_as_uint(gv) >> 23) & 0xffu);  // biased
-            e = e < 37 ? 37 : e > 253 ? 253 : e;
+            e = e < 37 ? 37 : e < 254 ? e : e == 255 ? 127 : 253;  // NaN in the weights alone, not in their base
             down[u][r] = __uint_as_float((uint32_t)(254 - e) << 23);
             ratio[u][r] = in ? gv * down[u][r] : 0.f;
             const float ef = __uint_as_float(0x4b000000u + (uint32_t)e) - (8388608.f + 127.f);
@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
         const int col = 8 * n + 2 * j + i;
         if (2 * j >= GW || col >= nheads) continue;
         const size_t bh = (size_t)piece.b * a.Hq + head0 + col;
-        const float inv = !whole ? 1.f : l[n][i] > 0.f ? 1.f / l[n][i] : 0.f;
+        const bool some = l[n][i] != 0.f;  // sees a token; a NaN among its scores is one in l, and stays one
+        const float inv = !whole ? 1.f : some ? 1.f / l[n][i] : 0.f;
         auto value = [&](int c) {  // feature number c of this lane
           const float up = 33554432.f / (kL * (float)(1 << VC::place(c)));
           return fmaf(acc[n][c >> 1][2 * (c & 1) + i], up, -wsum[n][i]) * inv;
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
             slot[a.group * D + col] = m[n][i];
             slot[a.group * D + a.group + col] = l[n][i];
           } else if (a.lse) {
-            a.lse[bh] = l[n][i] > 0.f ? (m[n][i] + log2f(l[n][i])) * 0.69314718055994530942f : -INFINITY;
+            a.lse[bh] = some ? (m[n][i] + log2f(l[n][i])) * 0.69314718055994530942f : -INFINITY;
           }
         }
       }
@@ -862,9 +863,9 @@ __global__ void __launch_bounds__(THREADS) attn_decode_join_kernel(const DecodeA
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) y += parts[i][threadIdx.x];
-    a.O[bh * D + threadIdx.x] = (uint16_t)(pack_bf16(sum > 0.f ? y / sum : 0.f, 0.f) & 0xffffu);
+    a.O[bh * D + threadIdx.x] = (uint16_t)(pack_bf16(sum != 0.f ? y / sum : 0.f, 0.f) & 0xffffu);
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[bh] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+  if (threadIdx.x == 0 && a.lse) a.lse[bh] = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace hbl

@@ -315,7 +315,8 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
 
 /* Attention of one token per sequence over the cache (its own K and V already appended):
  *   o[b][h] = sum_t softmax_t(scale q . k~_t) v~_t over the first lens[b] tokens of sequence b, head h
- *   of Hq reading KV head h / (Hq / Hkv); lens[b] = 0 gives o = 0 and lse = -inf.
+ *   of Hq reading KV head h / (Hq / Hkv); lens[b] = 0 gives o = 0 and lse = -inf. A NaN in q or in a
+ *   scale of K makes the heads that meet it NaN, lse included; one in a scale of V makes their o NaN.
  *   Q       device bf16 (rotated), rows of q_stride elements, as in hbl_kv_append
  *   tables  device int32 [B][table_width]: the pages of each sequence in order; entries past
  *           ceil(lens[b] / page_size) are not read. A page number out of range leaves its tokens out

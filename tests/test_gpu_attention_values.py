@@ -59,3 +59,70 @@ def test_prompt_infinite_scores(D):
     O, lse = run_prompt(c)
     ref = prompt_rows(c, O, lse, 0)
     assert not torch.isnan(ref[1][:, 0]).any() and torch.isnan(ref[1][:, 1]).sum() == 110
+
+
+# ------------------------------------------------------------------------------------------- decode
+
+def decode_rows(c, o, lse, b):
+    """Sequence b of a decode case against 64 bits, NaN and all."""
+    n, page = c["lens_host"][b], c["page"]
+    k, v, ref = decode_ref(c, b)
+    fin = lambda x: torch.where(torch.isfinite(x), x, 0.0).abs()
+    score_err, extra = 0.0, 0.0
+    if n:
+        # as in test_gpu_attention.check_decode: sums of D products of codes and q, then minus L sum q
+        score_err = float(3 * fin(c["Q"][b].double()).sum(-1).max() * fin(k).max() * abs(c["scale"]) *
+                          (c["D"] / 16 + 4) * 2.0 ** -23)
+        # weights below fp16's normal range are off by half its smallest step, 2^-25 where the largest product
+        # p gamma is 2^6 at least
+        rows = [c["tables"][b, j // page] * page + j % page for j in range(n)]
+        g = fin(torch.from_numpy(c["parts"][3][rows].astype(np.float64)).cuda()).amax(0)
+        extra = n * 2.0 ** -31 * g.repeat_interleave(c["Hq"] // c["Hkv"])[None, :, None] * \
+            torch.nan_to_num(ref[3][..., None], nan=0.0)
+    check_rows(o[b:b + 1], lse[b:b + 1], ref, 2.0 ** -11, score_err, extra)
+    return ref
+
+
+def with_records(c, change):
+    """The case with its cache's codes and scales changed in place by change(uk, uv, gk, gv, rows of sequence b)."""
+    page = c["page"]
+
+    def rows(b):
+        return np.array([c["tables"][b, j // page] * page + j % page for j in range(c["lens_host"][b])], np.int64)
+
+    change(*c["parts"], rows)
+    c["cache"] = torch.from_numpy(join_records(*c["parts"], c["bits"], page)).cuda()
+    return c
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bits", [(2, 2, 128, 3), (4, 2, 64, 2), (8, 2, 128, 4), (10, 2, 128, 8), (24, 2, 64, 3),
+                                           (6, 2, 256, 3)])
+@pytest.mark.parametrize("n", [40, 5000])
+def test_decode_keeps_nan(Hq, Hkv, D, bits, n):
+    """NaN in q, in a K scale or in a V scale: the same answer whether one warp holds the sequence or many."""
+    c = decode_case([n, n, n, n], Hq, Hkv, D, bits, 16, seed=n + D, dirty=False)
+    c["Q"][0, Hq - 1, 3] = NAN
+    c["Q"][0, 0] = NAN
+
+    def change(uk, uv, gk, gv, rows):
+        gk[rows(1)[n // 2], Hkv - 1] = NAN
+        gv[rows(2)[n // 3], 0] = NAN
+
+    with_records(c, change)
+    o, lse = run_decode(c)
+    refs = [decode_rows(c, o, lse, b) for b in range(4)]
+    G = Hq // Hkv
+    assert torch.isnan(refs[0][1]).sum() == 2
+    assert torch.isnan(refs[1][1]).sum() == G
+    assert not torch.isnan(refs[2][1]).any() and torch.isnan(refs[2][0]).sum() == G * D
+    assert hbl.hbl_device_status() == hbl.HBL_OK
+
+
+def test_decode_norms_at_scaled_values():
+    """The norm of the error in the outputs' own scale, whatever V's."""
+    for low, high in ((1e-20, 1e-20), (1e20, 1e20), (1.0, 1e25), (1e30, 1e36), (1e-12, 1e12)):
+        c = decode_case([500, 77], 8, 2, 128, 3, 32, seed=14, dirty=False, gv=lambda rng, g: np.where(
+            rng.random(g.shape) < 0.3, high * g, low * g).astype(np.float32))
+        o, lse = run_decode(c)
+        for b in range(2):
+            decode_rows(c, o, lse, b)
