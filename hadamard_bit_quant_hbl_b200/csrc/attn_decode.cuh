@@ -17,6 +17,9 @@
 // down to 2^-20 of the largest). scale gammaK (2 S - L sum q) / L gives the score; gammaV goes into
 // the weights w = p gammaV, rounded to fp16, whose largest is kept within fp16's range by running the
 // softmax's maximum over s + log2 of gammaV's binade; o = (2 O - L sum w) / (L sum p). Sums are fp32.
+// Codes are positive, so O and L sum w grow with the number of tokens while their difference does not, and a
+// tensor core's sum drops what lies below its last bits: summed over 131072 tokens and subtracted at the end, o
+// was off by 1 to 6%. L sum w / 2 is therefore taken off O every 64 tokens (1 to 3% of the time).
 // mma.sync does these products at the copy's pace (one 16x8x16 product per 256 codes) and takes A
 // from registers, where the masks leave it; tcgen05 would take 128-row tiles of shared or tensor
 // memory for at most 16 useful columns.
@@ -325,6 +328,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
   constexpr int CH = Cfg::kChunks, ST = Cfg::kStages, TILES = D / 16;
   constexpr int GW = 8 / R;                        // columns of a group
   constexpr int SUB = R == 1 && CH > 1 ? 2 : 1;    // softmax passes between checks of the maximum
+  constexpr int EVERY = 64 / Cfg::kBlock;          // blocks between two subtractions of the codes' middle
   static_assert(CH % (R * SUB) == 0 && (R == 1 || NT == 1), "");
   constexpr float kL = (float)((1 << BITS) - 1);
   extern __shared__ __align__(128) uint8_t dec_smem[];
@@ -556,7 +560,8 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
     }
 
     float acc[NT][TILES][4];
-    float wsum[NT][4];  // sums of the rounded weights: a product with ones, every row of it the same
+    float wsum[NT][4];  // sums of the rounded weights since the last subtraction: a product with ones, every row
+                        // of it the same
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -698,6 +703,22 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
           }
         }
       }
+      if (EVERY == 1 || at % EVERY == EVERY - 1 || at + 1 == piece.j1) {  // less L/2 of the weights so far
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const F2 w(wsum[n][0], wsum[n][1]);
+#pragma unroll
+          for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float half = kL * (float)(1 << VC::place(2 * t + i)) / 33554432.f;
+              float* x = &acc[n][t][2 * i];
+              fma2(w, F2(-half, -half), F2(x[0], x[1])).split(x[0], x[1]);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) wsum[n][i] = 0.f;
+        }
+      }
       __syncwarp();  // every lane is done with the stage
       copies.use();
       copy(st);
@@ -726,7 +747,6 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
             for (int o = GW / 2; o < 4; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
           };
           sum(l[n][i]);
-          sum(wsum[n][i]);
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
             sum(acc[n][t][i]);
@@ -740,7 +760,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
         const float inv = !whole ? 1.f : some ? 1.f / l[n][i] : 0.f;
         auto value = [&](int c) {  // feature number c of this lane
           const float up = 33554432.f / (kL * (float)(1 << VC::place(c)));
-          return fmaf(acc[n][c >> 1][2 * (c & 1) + i], up, -wsum[n][i]) * inv;
+          return acc[n][c >> 1][2 * (c & 1) + i] * up * inv;
         };
         constexpr int RUN = VC::kShared ? 1 : BITS == 8 ? 2 : 4;  // consecutive features
 #pragma unroll

@@ -118,6 +118,18 @@ def test_decode_keeps_nan(Hq, Hkv, D, bits, n):
     assert hbl.hbl_device_status() == hbl.HBL_OK
 
 
+@pytest.mark.parametrize("D,bits", [(128, 3), (64, 8), (128, 4)])
+def test_decode_long_pieces(D, bits):
+    """Sums over very many tokens: with as many sequences as warps, over the same pages, a warp holds 131072."""
+    c = decode_case([131072], 1, 1, D, bits, 64, seed=D + bits, dirty=False)
+    B = 1776
+    many = dict(c, Q=c["Q"].expand(B, 1, D).contiguous(), t=c["t"].expand(B, -1).contiguous(),
+                lens=c["lens"].expand(B).contiguous())
+    o, lse = run_decode(many)
+    for b in (0, 700, 1775):
+        decode_rows(c, o[b:b + 1], lse[b:b + 1], 0)
+
+
 def test_decode_norms_at_scaled_values():
     """The norm of the error in the outputs' own scale, whatever V's."""
     for low, high in ((1e-20, 1e-20), (1e20, 1e20), (1.0, 1e25), (1e30, 1e36), (1e-12, 1e12)):
