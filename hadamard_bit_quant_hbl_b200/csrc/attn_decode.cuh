@@ -15,8 +15,10 @@
 //
 // q is scaled per head by a power of two to [2^14, 2^15) and rounded to fp16 (exact for bf16 values
 // down to 2^-20 of the largest). scale gammaK (2 S - L sum q) / L gives the score; gammaV goes into
-// the weights w = p gammaV, rounded to fp16, whose largest is kept within fp16's range by running the
-// softmax's maximum over s + log2 of gammaV's binade; o = (2 O - L sum w) / (L sum p). Sums are fp32.
+// the weights w = p gammaV, rounded to fp16, whose largest is kept between 2^6 and 2^15 by running the
+// softmax's base over s + log2 of gammaV's binade: a weight below 2^-20 of the largest is rounded to steps of
+// 2^-30 of it. (With a largest of 1 the steps were 2^-24, and 131072 tokens of 2^-25 each beside one of 1 vanished.)
+// o = (2 O - L sum w) / (L sum p). Sums are fp32.
 // Codes are positive, so O and L sum w grow with the number of tokens while their difference does not, and a
 // tensor core's sum drops what lies below its last bits: summed over 131072 tokens and subtracted at the end, o
 // was off by 1 to 6%. L sum w / 2 is therefore taken off O every 64 tokens (1 to 3% of the time).
@@ -24,7 +26,7 @@
 // from registers, where the masks leave it; tcgen05 would take 128-row tiles of shared or tensor
 // memory for at most 16 useful columns.
 //
-// gammaV's binade runs from -90 to 126 (a zero counts as -90): p is at most 2^8, so p / 2^binade stays
+// gammaV's binade runs from -84 to 126 (a zero counts as -84): p is at most 2^13, so p / 2^binade stays
 // in range, and a weight that leaves fp32's range below belongs to a token whose gamma is 2^96 times
 // smaller than another's, or whose share is below 2^-30.
 //
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
             const float gk = reinterpret_cast<const float*>(rec + Rec::kGammaK)[row];
             const float gv = reinterpret_cast<const float*>(rec + Rec::kGammaV)[row];
             int e = (int)((__float_as_uint(gv) >> 23) & 0xffu);  // biased
-            e = e < 37 ? 37 : e < 254 ? e : e == 255 ? 127 : 253;  // NaN in the weights alone, not in their base
+            e = e < 43 ? 43 : e < 254 ? e : e == 255 ? 127 : 253;  // NaN in the weights alone, not in their base
             down[u][r] = __uint_as_float((uint32_t)(254 - e) << 23);
             ratio[u][r] = in ? gv * down[u][r] : 0.f;
             const float ef = __uint_as_float(0x4b000000u + (uint32_t)e) - (8388608.f + 127.f);
@@ -629,7 +631,8 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
                 z[u][n][2 * r + i] = in ? fmaf(gk, fmaf(cA[n][i], s[n][2 * r + i], -cB[n][i]), ef) : -INFINITY;
           }
         }
-        // the running maximum moves only when a weight would pass 2^8 (fp16 holds up to 2^16)
+        // the base m lies 2^6 below the largest product when it moves, and moves only when one would pass 2^13:
+        // with gammaV at up to four times its binade (in the last one) the weights stay below 2^15 (fp16: 2^16)
         bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -637,18 +640,19 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, D <= 128 && NT == 1 ? 3 : 2
           for (int i = 0; i < 2; ++i) {
             float top = fmaxf(z[0][n][i], z[0][n][2 + i]);
             if constexpr (SUB == 2) top = fmaxf(top, fmaxf(z[1][n][i], z[1][n][2 + i]));
-            grow |= top > m[n][i] + 8.f;
+            grow |= top > m[n][i] + 13.f;
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float top = m[n][i];
+              float top = -INFINITY;
 #pragma unroll
               for (int u = 0; u < SUB; ++u) top = fmaxf(top, fmaxf(z[u][n][i], z[u][n][2 + i]));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              top = fmaxf(m[n][i], top - 6.f);
               const float f = top == -INFINITY ? 1.f : ex2_approx(m[n][i] - top);
               m[n][i] = top;
               l[n][i] *= f;

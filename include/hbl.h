@@ -328,10 +328,11 @@ hbl_status hbl_kv_gather(const void* cache, size_t cache_bytes, int num_pages, i
  *           It needs no initial contents and keeps none between calls; calls that may overlap on the
  *           GPU need one each
  * Sums and softmax statistics are held in fp32; the weights times gamma_V are rounded to fp16 for the
- * product with V's codes. The gammas of V of a sequence and head may differ by a factor up to 2^96 (a
- * token whose gamma is smaller by more drops out of the sum of the weights too). The workspace holds one
- * part per warp of the device, whatever B: 1.9 MB for Hq = Hkv, times the query heads per KV head (16 at
- * most, 8 for D = 256), at D = 128.
+ * product with V's codes: each by at most 2^-11 of itself, or 2^-31 of the largest where that is more (so
+ * one below 2^-31 of the largest adds nothing to o, and still counts in the sum of the weights). The gammas
+ * of V of a sequence and head may differ by a factor up to 2^96 (a token whose gamma is smaller by more
+ * drops out of the sum of the weights too). The workspace holds one part per warp of the device, whatever
+ * B: 1.9 MB for Hq = Hkv, times the query heads per KV head (16 at most, 8 for D = 256), at D = 128.
  * B <= 4096; B = 0 does nothing. Grids do not depend on the lengths, so a captured call may be
  * replayed with other lengths, tables and cache contents. Asynchronous. */
 size_t hbl_attn_decode_workspace(int B, int Hq, int Hkv, int D);

@@ -2,7 +2,7 @@
 import torch
 
 
-def check_rows(o, lse, ref, weight_step, score_err, extra=0.0):
+def check_rows(o, lse, ref, weight_step, score_err, extra=0.0, sum_err=0.0):
     """o [n, H, D] and lse [n, H] against attn_ref.attention's result.
 
     NaN and -inf have to stand exactly where the 64-bit evaluation has them, and a row of lse = -inf is zero.
@@ -10,7 +10,8 @@ def check_rows(o, lse, ref, weight_step, score_err, extra=0.0):
     rounded to a type of half a step `weight_step` (of A = sum p |v|) and come from scores off by `score_err`
     (a factor of e^(2 score_err) after the normalisation); `extra`, in the outputs' scale, covers weights below
     the type's normal range. In the norm the two roundings are independent, each with a third of its half step's
-    square, and `extra` enters as the share of its own norm."""
+    square, and `extra` enters as the share of its own norm. `sum_err` is what the sum of the weights can be off
+    by, of itself."""
     ro, rlse, A, _ = ref
     o, lse = o.double(), lse.double()
     assert torch.equal(torch.isnan(o), torch.isnan(ro)), (int(torch.isnan(o).sum()), int(torch.isnan(ro).sum()))
@@ -29,5 +30,5 @@ def check_rows(o, lse, ref, weight_step, score_err, extra=0.0):
     fine = torch.isfinite(rlse)
     d = (lse - rlse)[fine].abs()
     if d.numel():
-        lim = score_err + 2.0 ** -17 + 2.0 ** -21 * rlse[fine].abs()
+        lim = score_err + sum_err + 2.0 ** -17 + 2.0 ** -21 * rlse[fine].abs()
         assert (d <= lim).all(), float((d / lim).max())

@@ -79,7 +79,9 @@ def decode_rows(c, o, lse, b):
         g = fin(torch.from_numpy(c["parts"][3][rows].astype(np.float64)).cuda()).amax(0)
         extra = n * 2.0 ** -31 * g.repeat_interleave(c["Hq"] // c["Hkv"])[None, :, None] * \
             torch.nan_to_num(ref[3][..., None], nan=0.0)
-    check_rows(o[b:b + 1], lse[b:b + 1], ref, 2.0 ** -11, score_err, extra)
+    # a lane adds the weights of its tokens, an eighth of a warp's, one after another: each sum is off by half a
+    # step, 2^-24 of it (a dominant token's lane drops all that lies below)
+    check_rows(o[b:b + 1], lse[b:b + 1], ref, 2.0 ** -11, score_err, extra, n / 8 * 2.0 ** -24)
     return ref
 
 
@@ -128,6 +130,36 @@ def test_decode_long_pieces(D, bits):
     o, lse = run_decode(many)
     for b in (0, 700, 1775):
         decode_rows(c, o[b:b + 1], lse[b:b + 1], 0)
+
+
+def dominant_case(n, below, bits=8, copies=1776):
+    """`copies` equal sequences over the same pages, so that a warp holds long pieces: n tokens whose weights are
+    2^-below of one more token's, which has the middle code (1/L of gamma) in its V where the others have gamma."""
+    D, page = 64, 64
+    L = (1 << bits) - 1
+    T = -(-(n + 1) // page) * page
+    uk = np.full((T, 1, D), L, np.int64)
+    uv = np.full((T, 1, D), L, np.int64)
+    uv[0] = (L + 1) // 2
+    gk = np.full((T, 1), 0.125, np.float32)
+    gk[0] = 0.125 + below * np.log(2.0) / 8  # score = gammaK * 64 / 8 at q = 1
+    gv = np.ones((T, 1), np.float32)
+    table = np.repeat(np.arange(T // page)[None], copies, 0)
+    Q = torch.ones((copies, 1, D), dtype=torch.bfloat16, device="cuda")
+    return dict(Q=Q, cache=torch.from_numpy(join_records(uk, uv, gk, gv, bits, page)).cuda(), t=i32(table),
+                lens=i32([n + 1] * copies), lens_host=[n + 1] * copies, parts=[uk, uv, gk, gv], tables=table, Hq=1, Hkv=1,
+                D=D, bits=bits, page=page, scale=0.125)
+
+
+@pytest.mark.parametrize("n,below", [(131071, 25.05), (131071, 24.8), (65535, 23.3), (131071, 20.0)])
+def test_decode_small_weights_beside_a_dominant_one(n, below):
+    """What very many small weights add up to: 2^-25 of the largest each, they come to as much as the
+    dominant token's own output. A weight is off by 2^-31 of the largest at most."""
+    c = dominant_case(n, below)
+    o, lse = run_decode(c)
+    assert (o == o[0]).all() or float((o - o[0]).abs().max()) < 2.0 ** -8 * float(o[0].abs().max())
+    for b in (0, 1, 888, 1775):
+        decode_rows(c, o, lse, b)
 
 
 def test_decode_norms_at_scaled_values():
