@@ -341,15 +341,23 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
             }
           }
         }
-        if (__any_sync(0xffffffffu, near)) {
-          // the heads of this warp once more (the other heads' codes come out the same)
+        const uint32_t nears = __ballot_sync(0xffffffffu, near);
+        if (nears != 0u) {
+          // once more in fp64: the heads that need it, and no other (whose gamma could differ in its last bits, so
+          // that a token's record depended on the heads that share its warp)
+          constexpr uint32_t kHead = 0xffffffffu >> (32 - LPH);  // the lanes of the first head
+          const bool again = (nears & (kHead << (hsub * LPH))) != 0u;
           float vs[8];
           uint32_t ys[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) vs[e] = v[e];
-          g = append_exact(vs, ys, LPH, kL, ROPE && kind < 2, ROPE ? a.pos[t0 + t] : 0, inv_freq + (ROPE ? 4 * sub : 0));
+          const float ge = append_exact(vs, ys, LPH, kL, ROPE && kind < 2, ROPE ? a.pos[t0 + t] : 0,
+                                        inv_freq + (ROPE ? 4 * sub : 0));
+          if (again) {
+            g = ge;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = ys[e];
+            for (int e = 0; e < 8; ++e) y[e] = ys[e];
+          }
         }
         // four codes side by side: the sums of the magic bits wrap to a constant
         constexpr uint32_t kSum = kAppendMagicBits * (1u + (1u << BITS) + (1u << (2 * BITS)) + (1u << (3 * BITS)));

@@ -170,3 +170,23 @@ def test_decode_norms_at_scaled_values():
         o, lse = run_decode(c)
         for b in range(2):
             decode_rows(c, o, lse, b)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 5, 7), (128, 4, 8), (128, 3, 5), (256, 2, 2)])
+@pytest.mark.parametrize("bits", [3, 8])
+def test_append_does_not_depend_on_the_call(D, Hq, Hkv, bits):
+    """A token's record is the same in one long prompt, in pieces of it and alone: heads share a warp with
+    other heads there."""
+    T, page = 2700, 16
+    _, _, (Q, K, V) = fused_states(T, Hq, Hkv, D, seed=D + bits)
+    pos = i32(np.random.default_rng(1).integers(0, 100000, T))
+    slots = i32(np.arange(T))
+    size = hbl.hbl_kv_cache_bytes(-(-T // page), page, Hkv, D, bits)
+    caches = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    hbl.hbl_kv_append(K, V, slots, caches[0], page, bits, pos=pos, Q=Q)
+    for a in range(0, T, 90):
+        hbl.hbl_kv_append(K[a:a + 90], V[a:a + 90], slots[a:a + 90], caches[1], page, bits, pos=pos[a:a + 90])
+    for a in range(T):
+        hbl.hbl_kv_append(K[a:a + 1], V[a:a + 1], slots[a:a + 1], caches[2], page, bits, pos=pos[a:a + 1], Q=Q[a:a + 1])
+    for cache in caches[1:]:
+        assert int((cache != caches[0]).sum()) == 0
