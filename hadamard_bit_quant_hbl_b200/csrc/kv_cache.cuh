@@ -80,6 +80,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// The larger of two values, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Two floats in one register pair: Blackwell's fp32 multiply-adds take two at a time.
 struct F2 {
   uint64_t v;
@@ -131,7 +138,8 @@ __device__ __forceinline__ void rope_cs(int pos, double inv_freq, float& c, floa
   s = fmaf(lo, c0, s0);
 }
 
-// The codes (plus the bits of kAppendMagic) and gamma of a lane's eight values of a head, all in 64 bits.
+// The codes (plus the bits of kAppendMagic) and gamma of a lane's eight values of a head, all in 64 bits; codes 0 and
+// gamma NaN for a head that is not finite.
 // Out of line: inlined, it and its sincos push the common path out of the instruction cache (8192 tokens of
 // 32 + 32 + 32 heads and their read-back 398 us against 236).
 constexpr float kAppendMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
@@ -140,8 +148,9 @@ constexpr uint32_t kAppendMagicBits = 0x4b400000u;
 static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, int lanes, float kL, bool turn, int pos,
                                                   const double* inv_freq) {
   double xd[8];
+  bool bad = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) xd[e] = (double)v[e];
+  for (int e = 0; e < 8; ++e) xd[e] = (double)v[e], bad |= !(fabsf(v[e]) < INFINITY);
   if (turn) {
 #pragma unroll 1
     for (int e = 0; e < 4; ++e) {
@@ -155,15 +164,18 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
   double gd = 0.0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) gd = fmax(gd, fabs(xd[e]));
-  for (int o = lanes / 2; o >= 1; o >>= 1) gd = fmax(gd, __shfl_xor_sync(0xffffffffu, gd, o));
+  for (int o = lanes / 2; o >= 1; o >>= 1) {
+    gd = fmax(gd, __shfl_xor_sync(0xffffffffu, gd, o));
+    bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
+  }
   const double L = (double)kL;
 #pragma unroll 1
   for (int e = 0; e < 8; ++e) {
     // a zero is L/2 whatever the rounding of L gamma
     const double code = gd > 0.0 && xd[e] != 0.0 ? rint((L * xd[e] + L * gd) / (2.0 * gd)) : rint(0.5 * L);
-    y[e] = kAppendMagicBits + (uint32_t)fmin(fmax(code, 0.0), L);
+    y[e] = kAppendMagicBits + (bad ? 0u : (uint32_t)fmin(fmax(code, 0.0), L));
   }
-  return (float)gd;
+  return bad ? NAN : (float)gd;
 }
 
 // One CTA takes 16 tokens and a range of heads, counted through Q, K and V; a warp takes 256 / D heads
@@ -297,9 +309,9 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
         if (!any_kv) continue;
         float g = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g = fmaxf(g, fabsf(w[e]));
+        for (int e = 0; e < 8; ++e) g = max_nan(g, fabsf(w[e]));
 #pragma unroll
-        for (int o = LPH / 2; o >= 1; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        for (int o = LPH / 2; o >= 1; o >>= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
         const float mult = g > 0.f ? 0.5f * kL * rcp_approx(g) : 0.f;
         uint32_t y[8];  // the code plus the magic bits
         float d[8], far = 0.f;
@@ -315,7 +327,7 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) far = fmaxf(far, fabsf(d[e]));
-        // in range, or the products may leave fp32's; written so that a NaN is not
+        // in range, or the products may leave fp32's; a NaN or an infinity is not
         const bool range = g == 0.f || (g > 1e-30f && g < 1e30f);
         bool near = kind != 0 && !(range && far <= 0.5f - kNear);
         if (near) {

@@ -190,3 +190,44 @@ def test_append_does_not_depend_on_the_call(D, Hq, Hkv, bits):
         hbl.hbl_kv_append(K[a:a + 1], V[a:a + 1], slots[a:a + 1], caches[2], page, bits, pos=pos[a:a + 1], Q=Q[a:a + 1])
     for cache in caches[1:]:
         assert int((cache != caches[0]).sum()) == 0
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 5), (128, 2, 3), (256, 1, 2)])
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("rope", [True, False])
+def test_append_marks_heads_that_are_not_finite(D, Hq, Hkv, bits, rope):
+    """A head with a NaN or an infinity gets the scale NaN: it reads back as NaN and makes the attention over
+    it NaN. The records of the heads around it are those without it."""
+    T, page = 40, 16
+    X, _, (Q, K, V) = fused_states(T, Hq, Hkv, D, seed=D + bits)
+    pos = i32(np.arange(T) * 17) if rope else None
+    size = hbl.hbl_kv_cache_bytes(3, page, Hkv, D, bits)
+    want, got = (torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    hbl.hbl_kv_append(K, V, i32(np.arange(T)), want, page, bits, pos=pos, Q=Q)
+    bad = {}  # (which, token, head)
+    for i, (t, value, where) in enumerate([(0, NAN, slice(3, 4)), (5, INF, slice(D - 1, D)), (15, -INF, slice(0, 1)),
+                                           (16, NAN, slice(None)), (31, INF, slice(None)), (39, NAN, slice(D // 2, None))]):
+        for x, which in ((K, 0), (V, 1)):
+            h = (i + which) % Hkv
+            x[t, h, where] = value
+            bad[which, t, h] = True
+    hbl.hbl_kv_append(K, V, i32(np.arange(T)), got, page, bits, pos=pos, Q=Q)
+    back, ref = (hbl.hbl_kv_gather(c, i32(np.arange(T)), Hkv, D, page, bits) for c in (got, want))
+    for which in (0, 1):
+        nan = torch.zeros((T, Hkv), dtype=torch.bool, device="cuda")
+        for w, t, h in bad:
+            if w == which:
+                nan[t, h] = True
+        assert torch.isnan(back[which][nan]).all()
+        assert torch.equal(back[which][~nan], ref[which][~nan])
+        # the scales, as they lie: NaN there and nowhere else
+        rec = got.view(-1, Hkv, 1, record_bytes(D, bits))[:, :, 0, 4 * D * bits + 64 * which:][:, :, :64]
+        g = rec.contiguous().view(torch.float32).transpose(1, 2).reshape(-1, Hkv)[:T]
+        assert torch.equal(torch.isnan(g), nan)
+    table = i32(np.arange(3)[None].repeat(2, 0))
+    q = torch.randn(2, Hkv, D, device="cuda").to(torch.bfloat16)
+    o = hbl.hbl_attn_decode(q, got, table, i32([T, 0]), Hkv, page, bits)
+    some = [any((w, t, h) in bad for w in (0, 1) for t in range(T)) for h in range(Hkv)]
+    for h in range(Hkv):
+        assert bool(torch.isnan(o[0, h]).all()) == some[h] and (o[1, h] == 0).all()
+    assert hbl.hbl_device_status() == hbl.HBL_OK
