@@ -118,18 +118,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// theta^(-2f / D) pos, less whole turns, in 64 bits: positions reach 2^31.
-__device__ __forceinline__ double rope_angle(int pos, double inv_freq) {
-  const double two_pi = 6.283185307179586476925;
+// The angle pos theta^(-2f / D), rounded to 64 bits, in turns less whole ones (|part| <= 1/2): the quotient by 2 pi
+// with its low part, off by 2^-53 of a turn for any position, where one rounded product loses 2^-53 of all the turns.
+__device__ __forceinline__ double rope_part(int pos, double inv_freq) {
+  constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;  // 1 / (2 pi)
   const double ang = (double)pos * inv_freq;
-  return ang - two_pi * rint(ang / two_pi);
+  const double turns = ang * hi;
+  return (turns - rint(turns)) + fma(ang, lo, fma(ang, hi, -turns));
 }
 
-// Its cosine and sine in fp32, off by at most 2^-24: the turn reduced in 64 bits, then sin and cos of its
-// leading 24 bits, turned on by the rest.
+// Its cosine and sine in fp32: those of the leading 24 bits of the part (off by a step, 2^-24 below 1), turned on by
+// the rest and rounded (half a step): off by 1.5 2^-24.
 __device__ __forceinline__ void rope_cs(int pos, double inv_freq, float& c, float& s) {
-  const double turns = (double)pos * inv_freq * 0.15915494309189533577;
-  const double part = turns - rint(turns);
+  const double part = rope_part(pos, inv_freq);
   const float hi = (float)part;
   const float lo = (float)(part - (double)hi) * 6.2831853071795865f;
   float s0, c0;
@@ -155,7 +156,7 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
 #pragma unroll 1
     for (int e = 0; e < 4; ++e) {
       double s, c;
-      sincos(rope_angle(pos, inv_freq[e]), &s, &c);
+      sincospi(2.0 * rope_part(pos, inv_freq[e]), &s, &c);
       const double x0 = (double)v[e], x1 = (double)v[4 + e];
       xd[e] = x0 * c - x1 * s;
       xd[4 + e] = x0 * s + x1 * c;
@@ -186,12 +187,12 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
 // another in the cache leave as whole sectors.
 //
 // A code is decided in fp32 unless the value lies within kNear of a .5 boundary, where L 2^-21 bounds
-// the error, in steps of 2^-23 L: 1.1 from the rotation and as much from gamma (cosine and sine off by
-// 2^-24, two roundings, of states up to sqrt(2) gamma), 0.75 from the reciprocal (one step) and its product,
-// 0.5 from the last sum. There the whole head is rotated, its gamma taken and its codes decided in fp64, so
-// that the codes are those of a 64-bit evaluation. A lane's eight values go two at a time through the
-// multiply-adds. Bound by latency and issue: 8192 tokens of 32 + 32 + 32 heads of 128 at three bits about
-// 105 us for 322 MB, 3.1 TB/s.
+// the error, in steps of 2^-23 L: 1.35 from the rotation and as much from gamma (cosine and sine off by
+// 1.5 2^-24, two roundings, of states up to sqrt(2) gamma), 0.75 from the reciprocal (one step) and its product,
+// 0.5 from the last sum, together 3.95 of 4. There the whole head is rotated, its gamma taken and its codes decided
+// in fp64, from the same angle (rope_part), so that the codes are those of a 64-bit evaluation at any position. A
+// lane's eight values go two at a time through the multiply-adds. Bound by latency and issue: 8192 tokens of
+// 32 + 32 + 32 heads of 128 at three bits about 105 us for 322 MB, 3.1 TB/s.
 template <int D, int BITS, bool ROPE>
 __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kernel(const KvAppendArgs a) {
   using Rec = KvRec<D, BITS>;
@@ -224,8 +225,8 @@ __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kerne
   const bool turn = ROPE && h_begin < a.Hq + Hkv;
 
   if (ROPE && turn) {
-    const double lt = log((double)a.theta);
-    for (int f = threadIdx.x; f < HALF; f += THREADS) inv_freq[f] = exp(-2.0 * (double)f / (double)D * lt);
+    // (exp(-2f / D log theta) would multiply the logarithm's rounding by up to its argument)
+    for (int f = threadIdx.x; f < HALF; f += THREADS) inv_freq[f] = pow((double)a.theta, -2.0 * (double)f / (double)D);
   }
   pdl_wait();  // the states may come from the kernel before this one
   pdl_launch_dependents();

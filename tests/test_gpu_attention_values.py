@@ -172,6 +172,16 @@ def test_decode_norms_at_scaled_values():
             decode_rows(c, o, lse, b)
 
 
+# ------------------------------------------------------------------------------------------- append
+
+def k_bytes(cache, Hkv, D, page):
+    """K codes [tokens, Hkv, D] at eight bits (a byte each) and the scales [tokens, Hkv], in slot order."""
+    rec = cache.view(-1, Hkv, page // 16, record_bytes(D, 8)).transpose(1, 2).reshape(-1, Hkv, record_bytes(D, 8))
+    k = rec[:, :, :16 * D].view(-1, Hkv, 16, D).transpose(1, 2).reshape(-1, Hkv, D)
+    g = rec[:, :, 32 * D:32 * D + 64].contiguous().view(torch.float32).transpose(1, 2).reshape(-1, Hkv)
+    return k.cpu().numpy(), g.cpu().numpy()
+
+
 @pytest.mark.parametrize("D,Hq,Hkv", [(64, 5, 7), (128, 4, 8), (128, 3, 5), (256, 2, 2)])
 @pytest.mark.parametrize("bits", [3, 8])
 def test_append_does_not_depend_on_the_call(D, Hq, Hkv, bits):
@@ -231,3 +241,65 @@ def test_append_marks_heads_that_are_not_finite(D, Hq, Hkv, bits, rope):
     for h in range(Hkv):
         assert bool(torch.isnan(o[0, h]).all()) == some[h] and (o[1, h] == 0).all()
     assert hbl.hbl_device_status() == hbl.HBL_OK
+
+
+def turned(x, pos, D, theta):
+    """RoPE in extended precision (a significand of 64 bits) of x [T, H, D]."""
+    half = D // 2
+    inv = np.longdouble(theta) ** (-2 * np.arange(half).astype(np.longdouble) / D)
+    ang = pos.astype(np.longdouble)[:, None] * inv
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    a, b = x[..., :half].astype(np.longdouble), x[..., half:].astype(np.longdouble)
+    return np.concatenate([a * c - b * s, a * s + b * c], -1), ang.astype(np.float64)
+
+
+def check_codes(u, g, x, pos, D, theta):
+    """Eight-bit codes and scales of x [T, H, D]. The angle of pair f is off by a step of theta^(-2f/D) in 64 bits
+    and half a step of its product, together 3/2 2^-52 of it (nothing at f = 0, where both are exact), and by
+    2^-49 for its reduction; a state moves by 2 gamma times that, and so does gamma. A code is the nearest whole
+    number unless a border lies within this distance."""
+    y, ang = turned(x, pos, D, theta)
+    L = 255
+    gamma = np.abs(y).max(-1)
+    t = (L * y + L * gamma[..., None]) / (2 * gamma[..., None])
+    e = 1.5 * 2.0 ** -52 * np.abs(ang)
+    e[:, 0] = 0
+    e = np.concatenate([e, e], -1)[:, None] + 2.0 ** -49
+    bound = L * (e + e.max(-1, keepdims=True)) + 2.0 ** -40
+    frac = t - np.floor(t)
+    near = np.abs(frac - 0.5) <= bound
+    d = u - np.rint(t).astype(np.int64)
+    tie = near | (x == 0)  # a zero is L/2 exactly, whose rounding the reference's gamma may tip
+    assert np.all(d[~tie] == 0), (int((d[~tie] != 0).sum()), d.size)
+    assert np.abs(d).max() <= 1
+    np.testing.assert_allclose(g, gamma.astype(np.float64), rtol=2.0 ** -21)
+
+
+def test_append_one_pair_at_far_positions():
+    """The pair whose angle is the position itself, which 64 bits hold exactly: codes are exact up to 2^31."""
+    T, H, D, page = 65536, 8, 64, 16
+    rng = np.random.default_rng(4)
+    x = np.zeros((T, H, D), np.float32)
+    x[:, :, 0], x[:, :, D // 2] = rng.standard_normal((2, T, H))
+    K = torch.from_numpy(x).cuda().to(torch.bfloat16)
+    x = K.float().cpu().numpy()
+    pos = rng.integers(2 ** 30, 2 ** 31, T)
+    pos[::8] = np.exp2(rng.uniform(0, 31, T // 8)).astype(np.int64)
+    pos[1::8] *= -1
+    cache = torch.zeros(hbl.hbl_kv_cache_bytes(T // page, page, H, D, 8), dtype=torch.uint8, device="cuda")
+    hbl.hbl_kv_append(K, K, i32(np.arange(T)), cache, page, 8, pos=i32(pos))
+    u, g = k_bytes(cache, H, D, page)
+    two = [0, D // 2]
+    check_codes(u[:, :, two].astype(np.int64), g, x[:, :, two], pos, 2, 10000.0)
+
+
+@pytest.mark.parametrize("low,high", [(0, 2 ** 17), (2 ** 24, 2 ** 25), (2 ** 27, 2 ** 28), (2 ** 30, 2 ** 31)])
+def test_append_codes_over_positions(low, high):
+    T, H, D, page = 2048, 4, 128, 16
+    rng = np.random.default_rng(low % 97)
+    K = torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).cuda().to(torch.bfloat16)
+    pos = rng.integers(low, high, T)
+    cache = torch.zeros(hbl.hbl_kv_cache_bytes(T // page, page, H, D, 8), dtype=torch.uint8, device="cuda")
+    hbl.hbl_kv_append(K, K, i32(np.arange(T)), cache, page, 8, pos=i32(pos), rope_theta=500000.0)
+    u, g = k_bytes(cache, H, D, page)
+    check_codes(u.astype(np.int64), g, K.float().cpu().numpy(), pos, D, 500000.0)
