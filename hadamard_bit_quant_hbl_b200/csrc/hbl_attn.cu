@@ -138,8 +138,8 @@ hbl_status launch_prompt(const PromptAttnArgs& a, cudaStream_t s) {
   long long tiles = a.total_q / tokens + a.B;
   const long long bound = (long long)a.B * ((a.max_q + tokens - 1) / tokens);
   if (bound < tiles) tiles = bound;
-  const long long grid = tiles * a.Hkv * a.groups;
-  if (grid == 0) return HBL_OK;
+  long long grid = tiles * a.Hkv * a.groups;
+  if (grid == 0) grid = 1;  // max_q = 0: the first CTA flags the sequences that have queries
   if (grid > 0x7fffffffll) return HBL_EUNSUPPORTED;
   return launch_pdl(k, dim3((unsigned)grid), dim3(Cfg::kThreads), Cfg::kSmem, s, mq, mk, mv, a);
 }

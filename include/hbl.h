@@ -301,8 +301,9 @@ size_t hbl_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D, int bits
  * T = 0 does nothing. The codes are those of an evaluation in 64 bits, at any position: the kernel decides
  * in fp32 and takes a head again in fp64 where a value lies within the fp32 error of a rounding boundary. (The
  * angle pos theta^(-2f/D) has 53 bits there, so two such evaluations may differ where a value lies within about
- * L |angle| 2^-51 of a boundary: 2 of 8.4 million eight-bit codes at positions from 2^30 to 2^31.) A head of K or V that holds a NaN or an infinity is stored with gamma NaN: it reads back
- * as NaN, and the attention over it is NaN. Asynchronous. */
+ * L |angle| 2^-51 of a boundary: 2 of 8.4 million eight-bit codes at positions from 2^30 to 2^31.) A head of
+ * K or V that holds a NaN or an infinity is stored with gamma NaN: it reads back as NaN, and the attention
+ * over it is NaN. Asynchronous. */
 hbl_status hbl_kv_append(const void* Q, size_t q_stride, const void* K, size_t k_stride, const void* V, size_t v_stride,
                          const int32_t* pos, const int32_t* slots, float rope_theta, int T, int Hq, int Hkv, int D,
                          int bits, void* cache, size_t cache_bytes, int num_pages, int page_size, void* q_out,

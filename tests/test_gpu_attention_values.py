@@ -303,3 +303,18 @@ def test_append_codes_over_positions(low, high):
     hbl.hbl_kv_append(K, K, i32(np.arange(T)), cache, page, 8, pos=i32(pos), rope_theta=500000.0)
     u, g = k_bytes(cache, H, D, page)
     check_codes(u.astype(np.int64), g, K.float().cpu().numpy(), pos, D, 500000.0)
+
+
+# ------------------------------------------------------------------------------------------- refusals
+
+def test_prompt_without_room_for_queries_is_flagged():
+    """A bound of no queries beside sequences that have some: flagged like any other bound that is too small."""
+    c = prompt_case([3, 20], [3, 40], 2, 1, 128, seed=1)
+    assert hbl.hbl_device_status() == hbl.HBL_OK
+    O, lse = run_prompt(c, max_q=0)
+    assert hbl.hbl_device_status() == hbl.HBL_EINVAL
+    assert (O == 9).all() and (lse == 9).all()
+    c["cq"] = np.zeros(3, np.int64)  # sequences without queries beside rows of none: nothing to leave out
+    O, lse = run_prompt(c, max_q=0)
+    assert hbl.hbl_device_status() == hbl.HBL_OK
+    assert (O == 9).all() and (lse == 9).all()
