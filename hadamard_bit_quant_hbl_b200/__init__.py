@@ -399,6 +399,8 @@ def _on(stream, dev: int):
     belongs to it: memory of another stream could be in use there, or be used again too early."""
     if isinstance(stream, int):
         stream = _torch.cuda.ExternalStream(stream, device=dev)
+    elif stream.device_index != dev:
+        raise ValueError("expected a stream of the tensors' device")
     return _torch.cuda.stream(stream)
 
 
