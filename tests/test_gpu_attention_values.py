@@ -318,3 +318,49 @@ def test_prompt_without_room_for_queries_is_flagged():
     O, lse = run_prompt(c, max_q=0)
     assert hbl.hbl_device_status() == hbl.HBL_OK
     assert (O == 9).all() and (lse == 9).all()
+
+
+def test_binding_refuses_one_wrong_argument():
+    """Calls that differ from a valid one in a single argument, each refused for that argument."""
+    d = decode_case([40, 17], 4, 2, 128, 3, 16, seed=1, dirty=False)
+    p = prompt_case([30], [30], 4, 2, 128, seed=1)
+    Q, K, V, cq, ck = p["Q"], p["K"], p["V"], i32(p["cq"]), i32(p["ck"])
+    T = K.shape[0]
+    slots, cache, t, lens = i32(np.arange(T)), d["cache"], d["t"], d["lens"]
+
+    def append(K=K, V=V, slots=slots, cache=cache, Q=Q, pos=None, q_out=None):
+        hbl.hbl_kv_append(K, V, slots, cache, 16, 3, pos=pos, Q=Q, q_out=q_out)
+
+    def gather(cache=cache, slots=slots, K=None, V=None):
+        hbl.hbl_kv_gather(cache, slots, 2, 128, 16, 3, K=K, V=V)
+
+    def decode(Q=d["Q"], cache=cache, t=t, lens=lens, O=None, lse=None):
+        hbl.hbl_attn_decode(Q, cache, t, lens, 2, 16, 3, O=O, lse=lse)
+
+    def prompt(Q=Q, K=K, V=V, cq=cq, ck=ck, O=None, lse=None):
+        hbl.hbl_attn_prompt(Q, K, V, cq, ck, O=O, lse=lse)
+
+    for f in (append, gather, decode, prompt):
+        f()
+    f32 = torch.zeros((2, 4), device="cuda")
+    for f, kw, why in (
+            (append, dict(K=K.float()), "bf16 K"), (append, dict(V=V.half()), "bf16 V"), (append, dict(Q=Q.float()), "bf16 Q"),
+            (append, dict(V=V[:-1]), "one shape"), (append, dict(K=K[:, :, ::2], V=V[:, :, ::2]), "dense heads in K"),
+            (append, dict(V=V[:, :, :64]), "dense heads in V"), (append, dict(Q=Q[:-1]), "tokens and the head size"),
+            (append, dict(q_out=Q[:, :2]), "shape of Q"), (append, dict(slots=slots[:-1]), "slots of"),
+            (append, dict(slots=slots.long()), "slots"), (append, dict(pos=slots[:-1]), "pos of"),
+            (append, dict(cache=cache.view(torch.int8)), "cache"), (append, dict(cache=cache[::2]), "cache"),
+            (append, dict(slots=slots.cpu()), "CUDA"), (append, dict(K=K.view(T, -1)), "tokens, heads, D"),
+            (gather, dict(K=K[:-1].contiguous()), "K of shape"), (gather, dict(V=V.float()), "contiguous"),
+            (gather, dict(slots=slots.long()), "slots"), (gather, dict(cache=cache.view(torch.int32)), "cache"),
+            (decode, dict(Q=d["Q"].float()), "bf16 Q"), (decode, dict(t=t[:1]), "tables"), (decode, dict(t=t[0]), "tables"),
+            (decode, dict(t=t.long()), "tables"), (decode, dict(lens=lens[:1]), "lens"), (decode, dict(lens=lens.float()), "lens"),
+            (decode, dict(O=d["Q"][:1].contiguous()), "O of shape"), (decode, dict(lse=f32.double()), "lse"),
+            (decode, dict(lse=f32[:1]), "lse of shape"), (decode, dict(lens=lens.cpu()), "CUDA"),
+            (prompt, dict(K=K[:-1]), "one shape"), (prompt, dict(K=K[:, :, :64], V=V[:, :, :64]), "dense heads in K"),
+            (prompt, dict(K=K[:, :, :64].contiguous(), V=V[:, :, :64].contiguous()), "head size of Q"),
+            (prompt, dict(ck=ck[:1]), "cu_k of"), (prompt, dict(cq=cq.long()), "cu_q"), (prompt, dict(O=Q[:-1].contiguous()), "O of shape"),
+            (prompt, dict(lse=f32), "lse of shape"), (prompt, dict(V=V.cpu()), "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            f(**kw)
+    assert hbl.hbl_device_status() == hbl.HBL_OK
