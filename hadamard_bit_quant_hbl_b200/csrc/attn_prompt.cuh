@@ -312,7 +312,9 @@ attn_prompt_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       // ---- a CTA number's tile pair, from where the last search ended (numbers mostly rise). Up to 32
       // sequences, causal: the pairs of most keys first, whatever their sequence (a level is a pair's place
       // counted in pairs from its sequence's first key), so that the last ones are short. Else one sequence
-      // after the other, 32 at a time.
+      // after the other, 32 at a time: a lane holds one sequence, and more of them have more pairs to end with.
+      // By level and by sequence, 32 heads on 8 of 128, 100 to 2400 tokens, us: 4 sequences 68, 74; 12 254, 259;
+      // 24 401, 409; 32 592, 604; of 1 to 600 tokens, 8 sequences 24, 26; 32 67, 73.
       const bool by_level = a.causal && a.B <= 32;
       int base_b = 0, base_tiles = 0;  // sequences and tile pairs before the current 32 (the current level)
       int level = -1, top_level = -1, q_b = 0, n_b = 0, k_b = 0, m_b = 0, low_b = 0, tiles_b = 0;  // of lane b

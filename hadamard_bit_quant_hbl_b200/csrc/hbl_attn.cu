@@ -88,9 +88,14 @@ hbl_status launch_decode_attn(DecodeAttnArgs a, cudaStream_t s) {
   if (want < grid) grid = (int)want;
   const hbl_status st = launch_pdl(k, dim3(grid), dim3(32 * kDecodeWarps), Cfg::kSmem, s, a);
   if (st != HBL_OK) return st;
-  // few heads have long chains: more threads read a chain's pieces at once
+  // Few heads have long chains: up to one CTA per SM, more threads read a chain's pieces at once. Whole calls with
+  // 1024 and with 256 threads, 32 heads on 8 of 128, us: one sequence of 131072 tokens (32 CTAs) 39.7, 41.5; one
+  // of 16 heads on 1 30.8, 57.1; four of 32768 (128) 39.2, 39.6; eight of 16384 (256) 42.3, 38.5; 64 of 4096 105.8,
+  // 67.9. (One of 500, short chains: 10.5, 9.4; the lengths are known to the device alone.)
   const dim3 joins((unsigned)(a.B * a.c.Hkv * a.groups), a.group);
-  return (long long)joins.x * joins.y <= 256
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return (long long)joins.x * joins.y <= device_sms(dev)
              ? launch_pdl(attn_decode_join_kernel<D, 1024>, joins, dim3(1024), 0, s, a)
              : launch_pdl(attn_decode_join_kernel<D, 256>, joins, dim3(256), 0, s, a);
 }
