@@ -191,8 +191,9 @@ static __device__ __noinline__ float append_exact(const float* v, uint32_t* y, i
 // 1.5 2^-24, two roundings, of states up to sqrt(2) gamma), 0.75 from the reciprocal (one step) and its product,
 // 0.5 from the last sum, together 3.95 of 4. There the whole head is rotated, its gamma taken and its codes decided
 // in fp64, from the same angle (rope_part), so that the codes are those of a 64-bit evaluation at any position. A
-// lane's eight values go two at a time through the multiply-adds. Bound by latency and issue: 8192 tokens of
-// 32 + 32 + 32 heads of 128 at three bits about 105 us for 322 MB, 3.1 TB/s.
+// lane's eight values go two at a time through the multiply-adds. No unit is full
+// (issue 54%, DRAM 21%): it waits for its states (4.3 long-scoreboard stalls an issue, two tokens of 16 bytes a lane
+// in flight). 8192 tokens of 32 + 32 + 32 heads of 128 at three bits 115 us for 322 MB, 2.8 TB/s.
 template <int D, int BITS, bool ROPE>
 __global__ void __launch_bounds__(kv_append_threads(D, BITS), 4) kv_append_kernel(const KvAppendArgs a) {
   using Rec = KvRec<D, BITS>;
@@ -518,9 +519,9 @@ __device__ __forceinline__ void store_32(uint16_t* p, const uint32_t* v) {
 
 // x~ = (2u - L) gamma / L, rounded to bf16. One CTA takes 16 tokens and passes their heads two at a time; a
 // thread takes 32 features of K or of V of one token, the lanes consecutive tokens, so that V's interleaved
-// units are read as whole sectors and every thread writes two. Writing 4 D bytes for D b / 4 + 8 read, it is
-// bound by the stores: 12.5 k tokens of 32
-// heads of 128 at three bits 57 us, 4.7 TB/s.
+// units are read as whole sectors and every thread writes two. It writes 4 D bytes for D b / 4 + 8 read, and what
+// it waits for are its reads (7.9 long-scoreboard stalls an issue, 1.9 of a full load-store queue; DRAM at 39% of
+// its peak in a single cold call): 12.5 k tokens of 32 heads of 128 at three bits 57 us, 4.7 TB/s.
 template <int D, int BITS>
 __global__ void __launch_bounds__(kGatherHeads * 2 * kGatherTokens * D / 32) kv_gather_kernel(const KvGatherArgs a) {
   using Rec = KvRec<D, BITS>;
